@@ -19,6 +19,10 @@ FMT_MXFP4_32 = 3
 DTYPE_F32 = 0
 DTYPE_F16 = 1
 DTYPE_BF16 = 2
+MX_FP4 = 1
+MX_FP8 = 2
+MX_ROWS = 0
+MX_TILES = 1
 DECODE_MAX_T = 16
 DEV_TIMEOUT = 0x1
 DEV_BOUNDS = 0x2
@@ -39,6 +43,7 @@ class QWeights(ctypes.Structure):
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _U64 = ctypes.c_uint64
+_I64 = ctypes.c_int64
 _F = ctypes.c_float
 _QW = ctypes.POINTER(QWeights)
 
@@ -66,6 +71,12 @@ _SIGS = {
     "moe_layer_workspace_size": (_U64, [_I, _I, _I, _QW, _QW]),
     "moe_layer_forward": (_I, [_P, _I, _P, _P, _I, _I, _QW, _QW, _F, _P, _P, _P, _P, _P, _U64,
                                _P, _P]),
+    "moe_mx_scale_bytes": (_U64, [_I, _I, _I]),
+    "moe_mx_quantize": (_I, [_P, _I, _I, _I, _I, _I64, _I64, _I, _P, _U64, _P, _I, _U64, _P]),
+    "moe_mx_dequantize": (_I, [_P, _U64, _P, _I, _U64, _I, _I, _I, _I, _P, _I, _I64, _I64, _P]),
+    "moe_mx_tile_scales": (_I, [_P, _I, _I, _P, _P]),
+    "moe_add_rmsnorm": (_I, [_P, _I, _P, _I, _P, _I, _I, _F, _P, _P, _I, _I, _P, _P, _I, _P]),
+    "moe_mx_linear": (_I, [_P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _I, _I64, _P, _P]),
 }
 
 _lib = None
@@ -246,3 +257,46 @@ def moe_layer_forward(x, T, w_router, bias, E, k, w: QWeights, shared: QWeights 
                                   _ptr(topk_ids_opt), _ptr(topk_w_opt), _ptr(workspace),
                                   ws_bytes, _ptr(dev_status), _stream(stream))
     return _check("moe_layer_forward", rc) if check else rc
+
+
+def moe_mx_scale_bytes(rows, K, scale_layout) -> int:
+    return int(load().moe_mx_scale_bytes(rows, K, scale_layout))
+
+
+def moe_mx_quantize(src, src_dtype, batch, rows, K, src_row_stride, src_batch_stride, fmt, codes,
+                    codes_batch_stride, scales, scale_layout, scales_batch_stride, stream=None,
+                    check=True):
+    rc = load().moe_mx_quantize(_ptr(src), src_dtype, batch, rows, K, src_row_stride,
+                                src_batch_stride, fmt, _ptr(codes), codes_batch_stride,
+                                _ptr(scales), scale_layout, scales_batch_stride, _stream(stream))
+    return _check("moe_mx_quantize", rc) if check else rc
+
+
+def moe_mx_dequantize(codes, codes_batch_stride, scales, scale_layout, scales_batch_stride, fmt,
+                      batch, rows, K, dst, dst_dtype, dst_row_stride, dst_batch_stride,
+                      stream=None, check=True):
+    rc = load().moe_mx_dequantize(_ptr(codes), codes_batch_stride, _ptr(scales), scale_layout,
+                                  scales_batch_stride, fmt, batch, rows, K, _ptr(dst), dst_dtype,
+                                  dst_row_stride, dst_batch_stride, _stream(stream))
+    return _check("moe_mx_dequantize", rc) if check else rc
+
+
+def moe_mx_tile_scales(scales, rows, K, tiles, stream=None, check=True):
+    rc = load().moe_mx_tile_scales(_ptr(scales), rows, K, _ptr(tiles), _stream(stream))
+    return _check("moe_mx_tile_scales", rc) if check else rc
+
+
+def moe_add_rmsnorm(x, x_dtype, delta, delta_dtype, gain, T, H, eps, residual_out, out, out_dtype,
+                    mx_fmt, codes, scales, scale_layout, stream=None, check=True):
+    rc = load().moe_add_rmsnorm(_ptr(x), x_dtype, _ptr(delta), delta_dtype, _ptr(gain), T, H, eps,
+                                _ptr(residual_out), _ptr(out), out_dtype, mx_fmt, _ptr(codes),
+                                _ptr(scales), scale_layout, _stream(stream))
+    return _check("moe_add_rmsnorm", rc) if check else rc
+
+
+def moe_mx_linear(x_codes, x_fmt, x_scales, T, w_codes, w_fmt, w_scales, N, K, bias, y, y_dtype,
+                  ldy, dev_status, stream=None, check=True):
+    rc = load().moe_mx_linear(_ptr(x_codes), x_fmt, _ptr(x_scales), T, _ptr(w_codes), w_fmt,
+                              _ptr(w_scales), N, K, _ptr(bias), _ptr(y), y_dtype, ldy,
+                              _ptr(dev_status), _stream(stream))
+    return _check("moe_mx_linear", rc) if check else rc

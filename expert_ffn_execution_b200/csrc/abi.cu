@@ -2,6 +2,7 @@
 // workspace carving and kernel launches.  See include/strata_moe.h.
 #include <algorithm>
 
+#include "abi_util.h"
 #include "decode.cuh"
 #include "scratch_cache.h"
 
@@ -10,25 +11,6 @@ using namespace strata;
 namespace {
 
 constexpr int kAbiVersion = 1;
-constexpr int kMaxDevices = 64;
-
-int num_sms_of_current_device() {
-  static int cache[kMaxDevices] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
-  if (cache[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-      n = 148;
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int32_t from_cuda(cudaError_t e) { return e == cudaSuccess ? STRATA_OK : STRATA_ECUDA; }
-
 uint64_t up256(uint64_t x) { return (x + 255) & ~uint64_t(255); }
 
 bool valid_weights(const strata_qweights* w) {
@@ -347,12 +329,6 @@ int32_t moe_combine(const void* y, int32_t y_dtype, const int32_t* inv, const fl
                                   H, out, residual_out, dev_status,
                                   reinterpret_cast<cudaStream_t>(stream)));
 }
-
-namespace {
-int dtype_bytes(int32_t dt) {
-  return dt == STRATA_DTYPE_F32 ? 4 : (dt == STRATA_DTYPE_F16 || dt == STRATA_DTYPE_BF16) ? 2 : 0;
-}
-}  // namespace
 
 extern "C" int32_t moe_gather_rows(const void* src, int32_t src_dtype, int32_t n_src, int32_t H,
                                    const int32_t* idx, int32_t div, int32_t n, void* dst,

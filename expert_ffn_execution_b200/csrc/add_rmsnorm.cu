@@ -1,0 +1,152 @@
+// add_rmsnorm.cu -- the residual's addition, root-mean-square norm and
+// microscaled output in one pass:
+//   r = x + delta;  h = r / sqrt(mean r^2 + eps) * gain;
+//   residual_out = r;  out = round(h);  codes, scales = MX(h).
+//
+// One CTA a row, the row in registers between the sum of squares and the
+// output, so every input is read once and every output written once: bound by
+// HBM for many rows, by the launch and one load-reduce-store chain for few.
+// Sums are fp32 in a fixed order (per thread, warp butterfly, warp partials).
+#include "mx.cuh"
+#include "tc05.cuh"
+
+namespace strata {
+
+namespace {
+
+constexpr int kNMaxThreads = 512;
+
+STRATA_DEVFN void load8_as(const void* p, int dt, int64_t i, float (&v)[8]) {
+  if (dt == STRATA_DTYPE_F32)
+    load8<STRATA_DTYPE_F32>(reinterpret_cast<const float*>(p) + i, v);
+  else if (dt == STRATA_DTYPE_F16)
+    load8<STRATA_DTYPE_F16>(reinterpret_cast<const uint16_t*>(p) + i, v);
+  else
+    load8<STRATA_DTYPE_BF16>(reinterpret_cast<const uint16_t*>(p) + i, v);
+}
+STRATA_DEVFN void store8_as(void* p, int dt, int64_t i, const float (&v)[8]) {
+  if (dt == STRATA_DTYPE_F32)
+    store8<STRATA_DTYPE_F32>(reinterpret_cast<float*>(p) + i, v);
+  else if (dt == STRATA_DTYPE_F16)
+    store8<STRATA_DTYPE_F16>(reinterpret_cast<uint16_t*>(p) + i, v);
+  else
+    store8<STRATA_DTYPE_BF16>(reinterpret_cast<uint16_t*>(p) + i, v);
+}
+
+// VPT groups of 8 elements a thread: group threadIdx.x + blockDim.x * j.
+template <int VPT>
+__global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a) {
+  __shared__ float red[kNMaxThreads / 32];
+  const int tid = threadIdx.x, nth = blockDim.x;
+  const int G = a.H / 8;
+  const int kt = (a.H + 127) / 128;
+  const int row = blockIdx.x;
+  pdl_wait_prior();
+  if (row < a.T) {
+    const int64_t base = (int64_t)row * a.H;
+    float r[VPT][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int g = tid + nth * j;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[j][i] = 0.f;
+      if (g < G) load8_as(a.x, a.x_dtype, base + 8 * g, r[j]);
+    }
+    if (a.delta) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int g = tid + nth * j;
+        if (g < G) {
+          float d[8];
+          load8_as(a.delta, a.delta_dtype, base + 8 * g, d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) r[j][i] += d[i];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int g = tid + nth * j;
+      if (a.residual_out && g < G) store8_as(a.residual_out, a.x_dtype, base + 8 * g, r[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(r[j][i], r[j][i], ss);
+    }
+    ss = warp_sum(ss);
+    if ((tid & 31) == 0) red[tid >> 5] = ss;
+    __syncthreads();
+    ss = 0.f;
+    for (int w = 0; w < nth / 32; ++w) ss += red[w];
+    const float inv = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int g = tid + nth * j;
+      float h[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = r[j][i] * inv;
+      if (a.gain && g < G) {
+        float w[8];
+        load8<STRATA_DTYPE_F32>(a.gain + 8 * g, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] *= w[i];
+      }
+      if (a.out && g < G) store8_as(a.out, a.out_dtype, base + 8 * g, h);
+      if (a.fmt) {
+        uint2 c;
+        uint32_t e;
+        if (a.fmt == STRATA_MX_FP4)
+          e = mx_encode8<STRATA_MX_FP4>(h, c);
+        else
+          e = mx_encode8<STRATA_MX_FP8>(h, c);
+        if (g < G) {
+          if (a.fmt == STRATA_MX_FP4)
+            reinterpret_cast<uint32_t*>(a.codes)[base / 8 + g] = c.x;
+          else
+            reinterpret_cast<uint2*>(a.codes)[base / 8 + g] = c;
+          if ((tid & 3) == 0) {
+            if (a.layout == STRATA_MX_TILES)
+              a.scales[mx_tile_byte(row, g / 4, kt)] = (uint8_t)e;
+            else
+              a.scales[(base + 8 * g) / kMxBlock] = (uint8_t)e;
+          }
+        }
+      }
+    }
+  }
+  // padding of the scale tiles: the last blocks of every row, and the rows
+  // behind the last
+  if (a.fmt && a.layout == STRATA_MX_TILES) {
+    for (int b = (row < a.T ? a.H / kMxBlock : 0) + tid; b < kt * kMxTileBlocks; b += nth)
+      a.scales[mx_tile_byte(row, b, kt)] = 0;
+  }
+}
+
+template <int VPT>
+cudaError_t launch_norm(const AddNormArgs& a, int rows, int threads, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(rows);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, add_rmsnorm_kernel<VPT>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t st) {
+  const int rows = a.fmt && a.layout == STRATA_MX_TILES
+                       ? (int)(mx_ceil(a.T, kMxTileRows) * kMxTileRows)
+                       : a.T;
+  const int G = a.H / 8;
+  const int vpt = G <= kNMaxThreads ? 1 : G <= 2 * kNMaxThreads ? 2 : 4;
+  const int threads = (((G + vpt - 1) / vpt) + 31) & ~31;
+  if (vpt == 1) return launch_norm<1>(a, rows, threads, st);
+  if (vpt == 2) return launch_norm<2>(a, rows, threads, st);
+  return launch_norm<4>(a, rows, threads, st);
+}
+
+}  // namespace strata

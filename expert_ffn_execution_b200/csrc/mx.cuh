@@ -1,0 +1,213 @@
+// mx.cuh -- microscaled (OCP MX v1.0) rows: blocks of 32 consecutive elements
+// with one E8M0 scale byte, elements E2M1 (two a byte, low nibble first) or
+// E4M3, and the internal interfaces of the calls that make and read them.
+#pragma once
+
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace strata {
+
+constexpr int kMxBlock = 32;
+// A scale tile: 128 rows x 4 blocks (128 elements of K), 512 bytes, in the
+// order in which the tensor core wants the scales in tensor memory: 32 lanes
+// of 16 bytes, lane = row % 32, then row / 32, then the block.
+constexpr int kMxTileRows = 128;
+constexpr int kMxTileBlocks = 4;
+constexpr int kMxTileBytes = kMxTileRows * kMxTileBlocks;
+
+__host__ __device__ inline int64_t mx_row_bytes(int fmt, int64_t K) {
+  return fmt == STRATA_MX_FP4 ? K / 2 : K;
+}
+__host__ __device__ inline int64_t mx_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ inline int64_t mx_scale_plane(int64_t rows, int64_t K, int layout) {
+  return layout == STRATA_MX_TILES
+             ? mx_ceil(rows, kMxTileRows) * mx_ceil(K, kMxTileBlocks * kMxBlock) * kMxTileBytes
+             : rows * (K / kMxBlock);
+}
+// Byte of (row, block) in a plane of `kt` scale tiles a row of tiles.
+__host__ __device__ inline int64_t mx_tile_byte(int row, int block, int kt) {
+  return ((int64_t)(row / kMxTileRows) * kt + block / kMxTileBlocks) * kMxTileBytes +
+         (row % 32) * 16 + (row / 32 % 4) * 4 + block % kMxTileBlocks;
+}
+
+// ---------------------------------------------------------------- 8 elements
+// Eight consecutive elements of a tensor of dtype DT at p (16-byte aligned).
+template <int DT>
+STRATA_DEVFN void load8(const void* p, float (&v)[8]) {
+  if constexpr (DT == STRATA_DTYPE_F32) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0];
+    const float4 b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == STRATA_DTYPE_BF16) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(u32_as_h2(w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+}
+
+// Two values rounded to nearest even in the 16-bit type DT, first one low.
+template <int DT>
+STRATA_DEVFN uint32_t pack2(float a, float b) {
+  if constexpr (DT == STRATA_DTYPE_BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return h2_as_u32(__floats2half2_rn(a, b));
+  }
+}
+
+template <int DT>
+STRATA_DEVFN void store8(void* p, const float (&v)[8]) {
+  if constexpr (DT == STRATA_DTYPE_F32) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
+                   pack2<DT>(v[6], v[7]));
+  }
+}
+
+// ---------------------------------------------------------------- one block
+// A block of 32 is held by four adjacent lanes, eight elements each; all 32
+// lanes of the warp call this.  Scale: floor(log2 m) is the exponent field of
+// the largest magnitude's bits (which order like the magnitudes, Inf and NaN
+// above every number), so e = field - emax, at least 0; subnormal m has field
+// 0 and lands on e = 0 as the clamp asks.  x * 2^(127-e) is exact but for
+// results below the smallest element, which round to zero either way.
+// Returns e; codes: FP4 in .x, FP8 in .x and .y.
+template <int FMT>
+STRATA_DEVFN uint32_t mx_encode8(const float (&v)[8], uint2& codes) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  codes = make_uint2(0u, 0u);
+  if (m >= 0x7f800000u) return 255u;  // Inf or NaN in the block: the block is NaN
+  constexpr int kEmax = FMT == STRATA_MX_FP4 ? 2 : 8;
+  const int e = max((int)(m >> 23) - kEmax, 0);
+  const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = make_float2(v[2 * i] * inv, v[2 * i + 1] * inv);
+    if constexpr (FMT == STRATA_MX_FP4) {
+      codes.x |= (uint32_t)__nv_cvt_float2_to_fp4x2(p, __NV_E2M1, cudaRoundNearest) << (8 * i);
+    } else {
+      const uint32_t c = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
+      if (i < 2)
+        codes.x |= c << (16 * i);
+      else
+        codes.y |= c << (16 * (i - 2));
+    }
+  }
+  return (uint32_t)e;
+}
+
+// 2^(e-127) in fp32 (2^-127 is a subnormal; 255 is NaN).
+STRATA_DEVFN float mx_scale_value(uint32_t e) {
+  return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
+}
+
+// Eight codes -> values; exact in fp32 down to 2^-136, the smallest E4M3
+// step under the smallest scale.
+template <int FMT>
+STRATA_DEVFN void mx_decode8(uint2 codes, uint32_t e, float (&v)[8]) {
+  const float s = mx_scale_value(e);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __half2_raw h;
+    if constexpr (FMT == STRATA_MX_FP4) {
+      h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(codes.x >> (8 * i)), __NV_E2M1);
+    } else {
+      const uint32_t w = i < 2 ? codes.x : codes.y;
+      h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (i & 1))), __NV_E4M3);
+    }
+    const float2 f = __half22float2(__half2(h));
+    v[2 * i] = f.x * s;
+    v[2 * i + 1] = f.y * s;
+  }
+}
+
+// ---------------------------------------------------------------- interfaces
+struct MxQuantArgs {
+  const void* src;
+  int src_dtype;
+  int64_t batch, rows, K;
+  int64_t row_stride, batch_stride;  // elements
+  int fmt;
+  uint8_t* codes;
+  uint64_t codes_stride;  // bytes between matrices
+  uint8_t* scales;
+  int layout;
+  uint64_t scales_stride;  // bytes between matrices
+};
+cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t st);
+
+struct MxDequantArgs {
+  const uint8_t* codes;
+  uint64_t codes_stride;
+  const uint8_t* scales;
+  int layout;
+  uint64_t scales_stride;
+  int fmt;
+  int64_t batch, rows, K;
+  void* dst;
+  int dst_dtype;
+  int64_t row_stride, batch_stride;  // elements
+};
+cudaError_t launch_mx_dequantize(const MxDequantArgs& a, cudaStream_t st);
+cudaError_t launch_mx_tile_scales(const uint8_t* src, int64_t rows, int64_t K, uint8_t* dst,
+                                  cudaStream_t st);
+
+struct AddNormArgs {
+  const void* x;
+  int x_dtype;
+  const void* delta;  // or nullptr
+  int delta_dtype;
+  const float* gain;  // or nullptr
+  int T, H;
+  float eps;
+  void* residual_out;  // dtype of x, or nullptr
+  void* out;           // or nullptr
+  int out_dtype;
+  int fmt;  // 0: no codes
+  uint8_t* codes;
+  uint8_t* scales;
+  int layout;
+};
+cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t st);
+
+struct MxLinearArgs {
+  const uint8_t* x_codes;
+  int x_fmt;
+  const uint8_t* x_scales;
+  int T;
+  const uint8_t* w_codes;
+  int w_fmt;
+  const uint8_t* w_scales;
+  int N, K;
+  const float* bias;  // or nullptr
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  int32_t* status;
+  int num_sms;
+};
+cudaError_t launch_mx_linear(const MxLinearArgs& a, cudaStream_t st);
+
+}  // namespace strata

@@ -28,6 +28,12 @@ class ExpertWeights:
     def num_experts(self) -> int:
         return self.blobs.shape[0]
 
+    def dequantize(self, dtype=torch.float32, stream=None):
+        """(gate, up, down) that MXFP4 blobs stand for, [E, I, H] twice and
+        [E, H, I] of `dtype`; the other formats are refused."""
+        from .mx import unpack_experts
+        return unpack_experts(self, dtype, stream)
+
 
 class MoELayer:
     """One routed-expert FFN layer: router W_r bf16 [H, E], optional bias fp32

@@ -363,6 +363,114 @@ STRATA_API int32_t moe_layer_forward(const float* x, int32_t T, const uint16_t* 
                           void* workspace, uint64_t ws_bytes,
                           int32_t* dev_status, void* stream);
 
+/* ---------------------------------------------------------------- microscaled operators
+ * Operators around the routed layer: the residual's addition with the norm
+ * and a quantised output, the quantiser itself, and the product of two
+ * quantised matrices (projections, dense layers, a vocabulary head).  The
+ * pages have no counterpart of them; they follow the OCP Microscaling (MX)
+ * v1.0 specification, whose MXFP4 the expert format STRATA_FMT_MXFP4_32 is.
+ *
+ * An MX matrix [rows, K], K a multiple of 32, is a plane of codes and a plane
+ * of scales.  Blocks are 32 consecutive elements of one row with one E8M0
+ * scale byte e, worth 2^(e-127); e = 255 is NaN and makes its block NaN.
+ *   codes   STRATA_MX_FP4: E2M1, uint8 [rows][K/2], the low nibble the even
+ *           element (the codes of STRATA_FMT_MXFP4_32);
+ *           STRATA_MX_FP8: E4M3, uint8 [rows][K].
+ *   scales  STRATA_MX_ROWS: uint8 [rows][K/32] (the scales of
+ *           STRATA_FMT_MXFP4_32 and of published checkpoints);
+ *           STRATA_MX_TILES: uint8 [ceil(rows/128)][ceil(K/128)][512], the
+ *           byte of row r, block b in tile (r/128, b/4) at
+ *           (r%32)*16 + (r/32%4)*4 + b%4.  The calls that write tiles write
+ *           0 to the bytes without a row or block.
+ * Quantising: for a block of largest magnitude m, with emax = 2 (FP4) or 8
+ * (FP8), s = floor(log2 m) - emax clamped to -127..127 (-127 for m = 0),
+ * e = s + 127, and an element is x / 2^s rounded to nearest even, saturated
+ * at 6 (FP4) or 448 (FP8), the sign of zero kept.  A block that holds an Inf
+ * or NaN gets e = 255 and codes 0.  The result is determined bit for bit.
+ * None of these calls releases its dependents early, so their outputs can be
+ * moe_combine's inv, topk_w or residual. */
+#define STRATA_MX_FP4 1
+#define STRATA_MX_FP8 2
+#define STRATA_MX_ROWS 0
+#define STRATA_MX_TILES 1
+
+/* Bytes of the scale plane of one [rows, K] matrix; 0 for rows < 0, K < 32,
+ * K % 32 != 0 or an unknown layout. */
+STRATA_API uint64_t moe_mx_scale_bytes(int32_t rows, int32_t K, int32_t scale_layout);
+
+/* Quantises `batch` matrices [rows, K]:
+ *   src     F32 / F16 / BF16 elements; element (b, r, k) at
+ *           src[b*src_batch_stride + r*src_row_stride + k] (strides in
+ *           elements, >= 0, each a multiple of 16 bytes; src 16-byte aligned)
+ *   codes   matrix b at codes + b*codes_batch_stride bytes, 16-byte aligned;
+ *           rows back to back
+ *   scales  matrix b at scales + b*scales_batch_stride bytes (tiles: 16-byte
+ *           aligned)
+ * The batch strides are not looked at for batch == 1; otherwise each is at
+ * least one matrix's bytes.  With the planes of an expert blob as the outputs
+ * and the blob stride as both batch strides one call writes that plane of
+ * every expert.
+ * Limits: K a multiple of 32; batch, rows >= 0 (0: no-op); batch * rows (for
+ * tiles, rows rounded up to 128) below 2^31, and the call's 8-element groups
+ * below 2^40. */
+STRATA_API int32_t moe_mx_quantize(const void* src, int32_t src_dtype, int32_t batch, int32_t rows,
+                        int32_t K, int64_t src_row_stride, int64_t src_batch_stride, int32_t fmt,
+                        void* codes, uint64_t codes_batch_stride, void* scales,
+                        int32_t scale_layout, uint64_t scales_batch_stride, void* stream);
+
+/* Reads `batch` matrices [rows, K] back: dst = code * 2^(e-127), exact in
+ * fp32 except where it leaves fp32's range, rounded once for F16 / BF16.
+ * Arguments and limits as in moe_mx_quantize with dst in the place of src;
+ * dst_row_stride >= K for rows > 1, and dst rows do not overlap. */
+STRATA_API int32_t moe_mx_dequantize(const void* codes, uint64_t codes_batch_stride,
+                          const void* scales, int32_t scale_layout, uint64_t scales_batch_stride,
+                          int32_t fmt, int32_t batch, int32_t rows, int32_t K, void* dst,
+                          int32_t dst_dtype, int64_t dst_row_stride, int64_t dst_batch_stride,
+                          void* stream);
+
+/* Scales from STRATA_MX_ROWS to STRATA_MX_TILES (both of one [rows, K]
+ * matrix): what a checkpoint's scales need once before moe_mx_linear reads
+ * them.  tiles 16-byte aligned, moe_mx_scale_bytes() bytes; rows == 0 is a
+ * no-op. */
+STRATA_API int32_t moe_mx_tile_scales(const void* scales, int32_t rows, int32_t K, void* tiles,
+                           void* stream);
+
+/* The residual's addition and the norm that follows it:
+ *   r = x + delta,  h = r / sqrt(mean(r^2) + eps) * gain    (fp32)
+ *   residual_out = r   (dtype of x; NULL: not written; may alias x)
+ *   out = h            (out_dtype; NULL: not written)
+ *   codes, scales = the MX form of h   (mx_fmt 0: not written)
+ * The norm is of r before its rounding to the dtype of x.
+ *   x [T,H], delta [T,H] or NULL: F32 / F16 / BF16;  gain fp32 [H] or NULL
+ *   (unit gain).  At least one of residual_out, out and the MX form is
+ *   written.  Where codes are written, scales [T, H/32] go in scale_layout.
+ * Limits: T >= 0 (0: no-op), H in 32..16384, a multiple of 8, of 32 where
+ * codes are written.  All pointers 16-byte aligned (scales by rows: any).
+ * The sum of squares is fp32 in a fixed order: the same bits on every run. */
+STRATA_API int32_t moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* delta,
+                        int32_t delta_dtype, const float* gain, int32_t T, int32_t H, float eps,
+                        void* residual_out, void* out, int32_t out_dtype, int32_t mx_fmt,
+                        void* codes, void* scales, int32_t scale_layout, void* stream);
+
+/* y[t,n] = sum_k x[t,k] w[n,k] (+ bias[n]), both matrices MX, fp32
+ * accumulation on the tensor cores, one rounding to y_dtype.
+ *   x  [T,K] codes (32-byte aligned) and scales in STRATA_MX_TILES (16-byte
+ *      aligned); w [N,K] likewise;  bias fp32 [N] or NULL
+ *   y  F32 / F16 / BF16, row t at y + t*ldy elements, ldy >= N; the elements
+ *      between N and ldy are not touched
+ *   (x_fmt, w_fmt): (FP4, FP4), (FP8, FP4), (FP8, FP8); (FP4, FP8) returns
+ *      STRATA_EUNSUPPORTED
+ *   dev_status may be NULL.
+ * A row of x or w with a NaN block gives NaN in its outputs.  The sums'
+ * order depends on (T, N, K), the formats and the device alone: the same
+ * bits on every run.  No workspace.
+ * Limits: T >= 0 (0: no-op) up to 2^22, N >= 1, K a multiple of 128, at least
+ * 128, N and K up to 2^24. */
+STRATA_API int32_t moe_mx_linear(const void* x_codes, int32_t x_fmt, const void* x_scales, int32_t T,
+                      const void* w_codes, int32_t w_fmt, const void* w_scales, int32_t N,
+                      int32_t K, const float* bias, void* y, int32_t y_dtype, int64_t ldy,
+                      int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

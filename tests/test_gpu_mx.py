@@ -1,0 +1,443 @@
+"""GPU tests of the microscaled operators against plain forms in 64 bits.
+
+Quantised codes and scales, and values read back, are compared bit for bit:
+the format determines them.  Tolerances elsewhere are counted in half steps
+(2^-8 for bf16, 2^-11 for fp16, 2^-24 for fp32) as each test derives."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import expert_ffn_execution_b200 as sm  # noqa: E402
+import oracle  # noqa: E402
+from tests import mx_reference as ref  # noqa: E402
+from tests.harness import OUT_REL_L2, check_routing, rel_l2_rows  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+HALF_STEP = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+FMTS = [sm.MX_FP4, sm.MX_FP8]
+LAYOUTS = [sm.MX_ROWS, sm.MX_TILES]
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def n64(t):
+    return t.double().cpu().numpy()
+
+
+def hard_rows(rows, K, dtype, seed):
+    """Normal values over many magnitudes, with blocks of zeros, of signed
+    zeros, of subnormals, of the type's largest, exact ties, powers of two and
+    their neighbours, Inf and NaN."""
+    g = gen(seed)
+    x = torch.randn(rows, K, device=DEV, generator=g)
+    x *= torch.exp2(torch.randint(-12, 13, (rows, K // 32, 1), device=DEV, generator=g).float()).expand(
+        -1, -1, 32).reshape(rows, K)
+    x = x.to(dtype)
+    b = x.view(-1, 32)
+    info = torch.finfo(dtype)
+    special = [torch.zeros(32), -torch.zeros(32), torch.full((32,), info.tiny), torch.full((32,), info.smallest_normal / 4),
+               torch.full((32,), info.max), torch.arange(32) * 0.25, torch.arange(32) * -0.125, torch.arange(32) * 14.0,
+               torch.tensor([2.0 ** (i - 16) for i in range(32)]), torch.full((32,), 4.0).index_fill(0, torch.tensor([5]), float("inf")),
+               torch.ones(32).index_fill(0, torch.tensor([31]), float("nan")),
+               torch.full((32,), 8.0).index_fill(0, torch.tensor([0]), 8.0 - 8 * info.eps)]
+    for i, v in enumerate(special):
+        if (3 * i + 1) < b.shape[0]:
+            b[3 * i + 1] = v.to(device=DEV, dtype=dtype)
+    return x
+
+
+def host_codes(q):
+    c = q.codes.cpu().numpy()
+    return ref.unpack(c.reshape(q.rows, -1), q.fmt)
+
+
+def assert_quantised(q, x):
+    codes, scales = ref.quantize(n64(x), q.fmt)
+    s = q.scales.cpu().numpy()
+    if q.layout == sm.MX_TILES:
+        assert np.array_equal(s, ref.tile_scales(scales))
+    else:
+        assert np.array_equal(s, scales)
+    assert np.array_equal(host_codes(q), codes)
+
+
+# ---------------------------------------------------------------- quantiser
+@pytest.mark.parametrize("rows,K", [(1, 32), (3, 96), (128, 128), (130, 160), (67, 2592)])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_quantize(dtype, fmt, layout, rows, K):
+    x = hard_rows(rows, K, dtype, 1 + rows)
+    assert_quantised(sm.mx_quantize(x, fmt, layout), x)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_strided_rows(fmt):
+    wide = hard_rows(37, 256, torch.bfloat16, 2)
+    x = wide[:, 64:160]
+    assert_quantised(sm.mx_quantize(x, fmt), x)
+    x = wide[::3, 96:256]
+    assert_quantised(sm.mx_quantize(x, fmt, sm.MX_ROWS), x)
+    row = wide[5:6].expand(9, 256)  # one row nine times: stride 0
+    assert_quantised(sm.mx_quantize(row, fmt), row)
+
+
+def test_quantize_leaves_the_rest():
+    """Rows behind the last, and bytes between batches, stay as they were."""
+    E, rows, K = 3, 5, 64
+    x = hard_rows(E * rows, K, torch.float32, 3).view(E, rows, K)
+    cs, ss = rows * 32 + 48, rows * 2 + 7
+    codes = torch.full((E * cs + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+    scales = torch.full((E * ss + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+    sm.moe_mx_quantize(x, sm.DTYPE_F32, E, rows, K, K, rows * K, sm.MX_FP4, codes, cs, scales, sm.MX_ROWS, ss)
+    c, s = codes.cpu().numpy(), scales.cpu().numpy()
+    for e in range(E):
+        rc, rs = ref.quantize(n64(x[e]), sm.MX_FP4)
+        assert np.array_equal(c[e * cs:][:rows * 32].reshape(rows, 32), ref.pack(rc, sm.MX_FP4))
+        assert np.array_equal(s[e * ss:][:rows * 2].reshape(rows, 2), rs)
+        assert (c[e * cs + rows * 32:(e + 1) * cs] == 0xA5).all()
+        assert (s[e * ss + rows * 2:(e + 1) * ss] == 0xA5).all()
+
+
+def test_quantize_nothing():
+    for layout in LAYOUTS:
+        q = sm.mx_quantize(torch.empty(0, 64, device=DEV), sm.MX_FP4, layout)
+        assert q.codes.shape == (0, 32) and q.scales.numel() == 0
+        assert q.dequantize().shape == (0, 64)
+
+
+# ---------------------------------------------------------------- read-back
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("fmt", FMTS)
+def test_dequantize_every_code(fmt, layout, dtype):
+    """Every code under scales from the smallest to the largest and NaN."""
+    n = 16 if fmt == sm.MX_FP4 else 256
+    exps = np.array([0, 1, 20, 100, 118, 127, 130, 141, 240, 254, 255], np.uint8)
+    codes = np.tile(np.arange(n, dtype=np.uint8), (len(exps), 256 // n))
+    scales = np.repeat(exps[:, None], 8, 1)
+    want = ref.dequantize(codes, scales, fmt)
+    stored = torch.from_numpy(ref.pack(codes, fmt)).to(DEV)
+    s = torch.from_numpy(scales).to(DEV)
+    q = sm.MXTensor(stored, s, fmt, len(exps), 256, sm.MX_ROWS)
+    if layout == sm.MX_TILES:
+        q = sm.mx_tile_scales(q)
+        assert np.array_equal(q.scales.cpu().numpy(), ref.tile_scales(scales))
+    got = q.dequantize(dtype).cpu()
+    # exact in fp32, then one rounding: torch's own from the exact fp64 value through fp32
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(want.astype(np.float32)).to(dtype)
+    assert np.array_equal(got.float().numpy(), want.float().numpy(), equal_nan=True)
+
+
+@pytest.mark.parametrize("rows,K", [(1, 32), (129, 160), (300, 1056)])
+def test_tile_scales(rows, K):
+    s = torch.randint(0, 256, (rows, K // 32), dtype=torch.uint8, device=DEV, generator=gen(4))
+    q = sm.MXTensor(torch.zeros(rows, K, dtype=torch.uint8, device=DEV), s, sm.MX_FP8, rows, K, sm.MX_ROWS)
+    assert np.array_equal(sm.mx_tile_scales(q).scales.cpu().numpy(), ref.tile_scales(s.cpu().numpy()))
+
+
+# ---------------------------------------------------------------- norm
+def norm64(x, delta, gain, eps):
+    r = n64(x) + (0 if delta is None else n64(delta))
+    h = r / np.sqrt((r * r).mean(-1, keepdims=True) + eps)
+    return r, h * (1 if gain is None else n64(gain))
+
+
+# fp32 steps of h: the addition (half a step), the sum of H squares (each thread adds up to 32
+# squares in turn, then 5 + 16 partial sums: under 64 half steps, halved by the root), the mean, eps,
+# root, division and two products (half a step each, together under 8).
+H_REL = (1 + 32 + 8) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("T,H", [(1, 32), (1, 2560), (3, 40), (5, 2592), (130, 4096), (2, 16384)])
+@pytest.mark.parametrize("xt,dt,ot", [(torch.float32, torch.bfloat16, torch.bfloat16),
+                                      (torch.bfloat16, torch.bfloat16, torch.float16),
+                                      (torch.float16, torch.float32, torch.float32),
+                                      (torch.float32, None, torch.bfloat16)])
+def test_norm(xt, dt, ot, T, H):
+    g = gen(T + H)
+    x = torch.randn(T, H, device=DEV, generator=g).to(xt)
+    delta = None if dt is None else torch.randn(T, H, device=DEV, generator=g).to(dt)
+    gain = 1 + 0.1 * torch.randn(H, device=DEV, generator=g) if T != 3 else None
+    n = sm.add_rmsnorm(x, delta, gain, 1e-5, out_dtype=ot)
+    r, h = norm64(x, delta, gain, 1e-5)
+    if delta is None:
+        assert n.residual is x
+    else:
+        # one fp32 addition, one rounding to the dtype of x
+        want = (x.float() + delta.float()).to(xt)
+        assert torch.equal(n.residual, want)
+    # r's rounding is relative to r, so where x and delta cancel h's error is relative to |x| + |delta|
+    size = np.abs(h)
+    if delta is not None:
+        k = np.abs(h) / np.maximum(np.abs(r), 1e-300)
+        size = np.maximum(size, k * (np.abs(n64(x)) + np.abs(n64(delta))))
+    assert n.out.dtype == ot
+    tol = HALF_STEP[ot] * np.abs(h) + H_REL * (1 + HALF_STEP[ot]) * size + 2.0 ** -25  # fp16 subnormals
+    assert (np.abs(n64(n.out) - h) <= tol).all()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,H", [(1, 32), (4, 2560), (131, 2592), (3, 16384)])
+def test_norm_quantised(T, H, fmt, layout):
+    """The codes are those of h to within h's own rounding: the scale is that
+    of a largest magnitude within H_REL of h's, every value within half a step
+    of h on that scale, or saturated."""
+    g = gen(T * H)
+    x = torch.randn(T, H, device=DEV, generator=g)
+    delta = torch.randn(T, H, device=DEV, generator=g).bfloat16()
+    x[:, : min(H, 4)] *= 30
+    gain = 1 + 0.1 * torch.randn(H, device=DEV, generator=g)
+    n = sm.add_rmsnorm(x, delta, gain, 1e-6, out_dtype=torch.float32, fmt=fmt, layout=layout)
+    # the codes are the format's of the fp32 rows that `out` holds, bit for bit
+    assert_quantised(n.mx, n.out)
+    r, h = norm64(x, delta, gain, 1e-6)
+    size = np.abs(h) / np.maximum(np.abs(r), 1e-300) * (np.abs(n64(x)) + np.abs(n64(delta)))
+    assert (np.abs(n64(n.out) - h) <= (H_REL + 2.0 ** -24) * size).all()
+    only = sm.add_rmsnorm(x, delta, gain, 1e-6, fmt=fmt, layout=layout)
+    assert only.out is None and torch.equal(only.mx.codes, n.mx.codes) and torch.equal(only.mx.scales, n.mx.scales)
+
+
+def test_norm_in_place_and_zero_rows():
+    x = torch.randn(6, 256, device=DEV, generator=gen(5))
+    x[2] = 0
+    d = torch.randn(6, 256, device=DEV, generator=gen(6))
+    d[2] = 0
+    want = sm.add_rmsnorm(x, d, out_dtype=torch.bfloat16, fmt=sm.MX_FP8)
+    y = x.clone()
+    got = sm.add_rmsnorm(y, d, out_dtype=torch.bfloat16, fmt=sm.MX_FP8, residual_out=y)
+    assert got.residual is y and torch.equal(y, want.residual) and torch.equal(got.out, want.out)
+    assert (want.out[2] == 0).all() and (want.mx.dequantize()[2] == 0).all()
+    x[4, 7] = float("nan")
+    n = sm.add_rmsnorm(x, d, out_dtype=torch.float32, fmt=sm.MX_FP4)
+    assert n.out[4].isnan().all() and n.mx.dequantize()[4].isnan().all()
+    assert torch.equal(n.mx.codes[:4], sm.mx_quantize(n.out, sm.MX_FP4).codes[:4])
+    assert not n.out[[0, 1, 3, 5]].isnan().any()
+
+
+def test_norm_matches_the_layers_norm():
+    """Without delta and gain: within a step of moe_rmsnorm (bf16)."""
+    x = torch.randn(9, 2560, device=DEV, generator=gen(7))
+    a = torch.empty(9, 2560, dtype=torch.bfloat16, device=DEV)
+    sm.moe_rmsnorm(x, 9, 2560, 1e-6, a)
+    b = sm.add_rmsnorm(x, out_dtype=torch.bfloat16).out
+    assert ((a.float() - b.float()).abs() <= 2.0 ** -7 * a.float().abs()).all()
+
+
+# ---------------------------------------------------------------- product
+PAIRS = [(sm.MX_FP8, sm.MX_FP4), (sm.MX_FP4, sm.MX_FP4), (sm.MX_FP8, sm.MX_FP8)]
+
+
+def random_mx(rows, K, fmt, seed, lo=120, hi=130):
+    g = gen(seed)
+    if fmt == sm.MX_FP4:
+        codes = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device=DEV, generator=g)
+    else:
+        codes = torch.randint(0, 127, (rows, K), dtype=torch.uint8, device=DEV, generator=g)
+        codes |= torch.randint(0, 2, (rows, K), dtype=torch.uint8, device=DEV, generator=g) << 7
+    s = torch.randint(lo, hi, (rows, K // 32), dtype=torch.uint8, device=DEV, generator=g)
+    q = sm.MXTensor(codes, s, fmt, rows, K, sm.MX_ROWS)
+    v = torch.from_numpy(ref.dequantize(host_codes(q), s.cpu().numpy(), fmt)).to(DEV)
+    return sm.mx_tile_scales(q), v
+
+
+def assert_product(y, xv, wv, bias=None):
+    """|error| <= one rounding of the result + the fp32 sum's: products of codes are exact, an
+    instruction adds 32 or 64 of them and the sum so far, each kept to 24 bits of the largest: at most
+    K/32 + 64 truncations (a whole fp32 step each, 2^-23) of at most sum |x w|, and 8 joined parts and
+    a bias."""
+    want = xv @ wv.T
+    mag = xv.abs() @ wv.abs().T
+    if bias is not None:
+        want = want + bias.double()
+        mag = mag + bias.double().abs()
+    steps = xv.shape[1] / 32 + 64 + 9
+    tol = HALF_STEP[y.dtype] * want.abs() + steps * 2.0 ** -23 * mag + (2.0 ** -25 if y.dtype == torch.float16 else 0)
+    bad = ~((y.double() - want).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:5].tolist(), float((y.double() - want).norm() / want.norm()))
+
+
+SHAPES = [(1, 128, 128), (1, 1, 128), (3, 100, 256), (16, 129, 384), (17, 300, 640), (33, 128, 1024), (64, 127, 128),
+          (65, 257, 512), (128, 128, 128), (129, 385, 896), (300, 641, 2688), (513, 1000, 256), (4, 4100, 2560),
+          (2, 40000, 128), (8, 64, 16384)]
+
+
+@pytest.mark.parametrize("xf,wf", PAIRS)
+@pytest.mark.parametrize("T,N,K", SHAPES)
+def test_linear(T, N, K, xf, wf):
+    x, xv = random_mx(T, K, xf, T + N)
+    w, wv = random_mx(N, K, wf, T + N + 1)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = sm.mx_linear(x, w, out_dtype=torch.float32, dev_status=status)
+    assert sm.strata_read_status(status) == 0
+    assert_product(y, xv, wv)
+
+
+@pytest.mark.parametrize("xf,wf", PAIRS)
+@pytest.mark.parametrize("T", [2, 200])
+def test_linear_is_exact_on_small_integers(T, xf, wf):
+    """Whole numbers whose sums stay below 2^24: no rounding anywhere."""
+    N, K = 200, 640
+    g = gen(T)
+    xi = torch.randint(-3, 4, (T, K), device=DEV, generator=g).float()
+    wi = torch.randint(-3, 4, (N, K), device=DEV, generator=g).float()
+    xi.view(T, -1, 32)[..., 0] = 4  # every block's largest is 4: scales of 1 (FP4)
+    wi.view(N, -1, 32)[..., 0] = 4
+    y = sm.mx_linear(sm.mx_quantize(xi, xf), sm.mx_quantize(wi, wf), out_dtype=torch.float32)
+    assert torch.equal(y.double(), xi.double() @ wi.double().T)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,N", [(5, 300), (150, 259)])
+def test_linear_bias_dtypes_and_row_stride(T, N, dtype):
+    K = 512
+    x, xv = random_mx(T, K, sm.MX_FP8, 1, 118, 122)
+    w, wv = random_mx(N, K, sm.MX_FP4, 2, 118, 122)
+    bias = torch.randn(N, device=DEV, generator=gen(3))
+    wide = torch.full((T + 2, N + 13), 7.0, dtype=dtype, device=DEV)
+    out = wide[1:-1, 3:N + 3]
+    got = sm.mx_linear(x, w, bias, out=out)
+    assert got is out
+    assert_product(out, xv, wv, bias)
+    wide[1:-1, 3:N + 3] = 7.0
+    assert (wide == 7.0).all()  # nothing else was written
+
+
+@pytest.mark.parametrize("xf,wf", PAIRS)
+@pytest.mark.parametrize("T", [4, 140])
+def test_linear_nan_blocks_stay_in_their_rows(T, xf, wf):
+    N, K = 140, 384
+    x, xv = random_mx(T, K, xf, 5)
+    w, wv = random_mx(N, K, wf, 6)
+    xs = x.scales.clone()
+    xs[(1 % 32) * 16 + 2] = 255       # row 1, block 2
+    ws = w.scales.clone()
+    ws[2 * 512 + (7 % 32) * 16 + 3] = 255  # row 7, block 11, the last
+    y = sm.mx_linear(sm.MXTensor(x.codes, xs, xf, T, K, sm.MX_TILES),
+                     sm.MXTensor(w.codes, ws, wf, N, K, sm.MX_TILES), out_dtype=torch.float32)
+    assert y[1].isnan().all() and y[:, 7].isnan().all()
+    keep_t = [t for t in range(T) if t != 1]
+    keep_n = [n for n in range(N) if n != 7]
+    assert_product(y[keep_t][:, keep_n].contiguous(), xv[keep_t], wv[keep_n])
+
+
+def test_linear_extreme_scales():
+    """Scale bytes far apart whose products are in fp32's range."""
+    T, N, K = 7, 130, 256
+    x, xv = random_mx(T, K, sm.MX_FP8, 8, 10, 12)
+    w, wv = random_mx(N, K, sm.MX_FP8, 9, 240, 242)
+    assert_product(sm.mx_linear(x, w, out_dtype=torch.float32), xv, wv)
+
+
+def test_linear_same_bits_every_time_and_in_any_batch_of_a_tile():
+    x, _ = random_mx(200, 1024, sm.MX_FP8, 10)
+    w, _ = random_mx(700, 1024, sm.MX_FP4, 11)
+    a = sm.mx_linear(x, w, out_dtype=torch.float32)
+    for _ in range(5):
+        assert torch.equal(a, sm.mx_linear(x, w, out_dtype=torch.float32))
+
+
+def test_linear_nothing():
+    w, _ = random_mx(64, 128, sm.MX_FP4, 12)
+    x = sm.mx_quantize(torch.empty(0, 128, device=DEV), sm.MX_FP8)
+    assert sm.mx_linear(x, w).shape == (0, 64)
+
+
+# ---------------------------------------------------------------- together
+def step(x, d, gain, w, out):
+    n = sm.add_rmsnorm(x, d, gain, fmt=sm.MX_FP8, residual_out=x)
+    return sm.mx_linear(n.mx, w, out=out)
+
+
+def test_two_graphs_and_a_side_stream():
+    """Steps captured in two graphs, replayed in turn, and run on another
+    stream, give the bits of the eager calls."""
+    T, H, N = 4, 2560, 1000
+    w, _ = random_mx(N, H, sm.MX_FP4, 13, 116, 120)
+    gain = torch.ones(H, device=DEV)
+    ins = [(torch.randn(T, H, device=DEV, generator=gen(20 + i)),
+            torch.randn(T, H, device=DEV, generator=gen(30 + i)).bfloat16()) for i in range(2)]
+    want = []
+    for x, d in ins:
+        r, o = x.clone(), torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+        step(r, d, gain, w, o)
+        want.append((r, o))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        r, o = ins[0][0].clone(), torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+        step(r, ins[0][1], gain, w, o)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(r, want[0][0]) and torch.equal(o, want[0][1])
+    held = []
+    for x, d in ins:
+        r, o = x.clone(), torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(r, d, gain, w, o)
+        held.append((g, r, o, x))
+    for _ in range(3):
+        for g, r, o, x in held:
+            r.copy_(x)
+            o.zero_()
+        for g, *_ in held:
+            g.replay()
+        for (g, r, o, x), (wr, wo) in zip(held, want):
+            assert torch.equal(r, wr) and torch.equal(o, wo)
+
+
+@pytest.mark.parametrize("T", [4, 48])
+def test_packed_experts_in_the_layer(T):
+    """bf16 weights -> blobs -> the MoE layer -> the norm after it -> a
+    projection: the blobs are the format's bit for bit, the layer agrees with
+    the oracle on them, and the projection with 64 bits on its own input."""
+    H, I, E, k, N = 512, 256, 16, 4, 300
+    g = gen(40)
+    gate, up = (0.05 * torch.randn(E, I, H, device=DEV, generator=g).bfloat16() for _ in range(2))
+    down = 0.05 * torch.randn(E, H, I, device=DEV, generator=g).bfloat16()
+    ex = sm.pack_experts(gate, up, down)
+    for t, v in zip((gate, up, down), ex.dequantize()):
+        c, s = ref.quantize(n64(t).reshape(-1, t.shape[2]), sm.MX_FP4)
+        assert np.array_equal(n64(v).reshape(c.shape), ref.dequantize(c, s, sm.MX_FP4))
+    x = torch.randn(T, H, device=DEV, generator=g)
+    wr = (0.02 * torch.randn(H, E, device=DEV, generator=g)).bfloat16()
+    layer = sm.MoELayer(wr, None, ex, k)
+    ids = torch.empty(T, k, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = layer.forward(x, topk_ids=ids, dev_status=status)
+    assert sm.strata_read_status(status) == 0
+    hid = oracle.rmsnorm(x.cpu().numpy())
+    wr16 = wr.cpu().view(torch.int16).numpy().view(np.uint16)
+    lg = oracle.router_logits(hid, wr16, None)
+    assert check_routing(lg, ids.cpu().numpy(), k)[0]
+    r = oracle.moe_layer(hid, wr16, None, E, k, sm.FMT_MXFP4_32, I, ex.blobs.cpu().numpy(),
+                         forced_ids=ids.cpu().numpy())
+    assert rel_l2_rows(out.float().cpu().numpy(), r["out_f32"]).max() <= OUT_REL_L2
+    n = sm.add_rmsnorm(x, out, fmt=sm.MX_FP8)
+    assert torch.equal(n.residual, x + out.float())
+    w, wv = random_mx(N, H, sm.MX_FP4, 41, 118, 122)
+    y = sm.mx_linear(n.mx, w, dev_status=status)
+    assert sm.strata_read_status(status) == 0
+    assert_product(y, n.mx.dequantize().double(), wv)
+
+
+@pytest.mark.parametrize("E,I,H", [(1, 128, 128), (5, 128, 384), (3, 640, 2560)])
+def test_pack_experts_strides(E, I, H):
+    """Weights whose experts or rows are further apart than they are long."""
+    g = gen(50)
+    gate = torch.randn(E, I, H + 16, device=DEV, generator=g).half()[:, :, 8:H + 8]
+    up = torch.randn(2 * E, I, H, device=DEV, generator=g)[::2]
+    down = torch.randn(E, H, I, device=DEV, generator=g).bfloat16()
+    blob = sm.pack_experts(gate, up, down)
+    assert blob.blobs.shape == (E, sm.strata_expert_bytes(sm.FMT_MXFP4_32, H, I))
+    for t, v in zip((gate, up, down), blob.dequantize(torch.bfloat16)):
+        c, s = ref.quantize(n64(t).reshape(-1, t.shape[2]), sm.MX_FP4)
+        assert np.array_equal(n64(v).reshape(c.shape), ref.dequantize(c, s, sm.MX_FP4))
