@@ -209,5 +209,6 @@ struct MxLinearArgs {
   int num_sms;
 };
 cudaError_t launch_mx_linear(const MxLinearArgs& a, cudaStream_t st);
+cudaError_t launch_mx_gemm(const MxLinearArgs& a, cudaStream_t st);
 
 }  // namespace strata

@@ -156,7 +156,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
             // two instructions share a scale column at K = 64, four at K = 32
             const int b = C::F4 ? j / 2 : 0;
             const uint32_t sf = C::F4 ? 2u * (j & 1) : (uint32_t)j;
-            mma_mx<C::F4>(tbase, wlo + 2 * j, xlo + 2 * j, hi, idesc_mx(wf, xf, NT, sf),
+            mma_mx<C::F4>(tbase, wlo + 2 * j, xlo + 2 * j, hi, idesc_mx(wf, xf, kLM, NT, sf),
                           sfw + 4 * b, sfx + 4 * b, (uint32_t)(i + j > 0));
           }
         }
@@ -166,8 +166,8 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     }
     __syncwarp();
   } else {
-    const bool ok = mbar_wait_guarded(tfull, 0, a.status, abort_flag) && !*abort_flag;
-    __syncwarp();
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_guarded(tfull, 0, a.status, abort_flag) &&
+                                                !*abort_flag);
     tc_fence_after();
     const int f = warp * 32 + lane;  // feature of the tile
     float* red = reinterpret_cast<float*>(smem);
@@ -278,7 +278,8 @@ cudaError_t launch_linear_t(const MxLinearArgs& a, cudaStream_t st) {
   if (a.T <= 16) return launch_linear<XF, WF, 16>(a, st);
   if (a.T <= 32) return launch_linear<XF, WF, 32>(a, st);
   if (a.T <= 64) return launch_linear<XF, WF, 64>(a, st);
-  return launch_linear<XF, WF, 128>(a, st);
+  if (a.T <= 128) return launch_linear<XF, WF, 128>(a, st);
+  return launch_mx_gemm(a, st);
 }
 
 }  // namespace
