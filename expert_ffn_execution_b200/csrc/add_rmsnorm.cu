@@ -16,13 +16,32 @@ namespace {
 
 constexpr int kNMaxThreads = 512;
 
-STRATA_DEVFN void load8_as(const void* p, int dt, int64_t i, float (&v)[8]) {
+// The row's groups of this thread, loaded before the first is used (the type
+// is looked at outside the loop, which leaves the loads free to overlap).
+template <int DT, int VPT>
+STRATA_DEVFN void load_groups(const void* p, int64_t base, int G, float (&v)[VPT][8]) {
+  constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
+  const uint8_t* b = reinterpret_cast<const uint8_t*>(p) + base * kEl;
+  Raw8<DT> raw[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int g = threadIdx.x + blockDim.x * j;
+    if (g < G)
+      raw[j].load(b + (int64_t)g * (8 * kEl));
+    else
+      raw[j].zero();
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) raw[j].values(v[j]);
+}
+template <int VPT>
+STRATA_DEVFN void load_groups_as(const void* p, int dt, int64_t base, int G, float (&v)[VPT][8]) {
   if (dt == STRATA_DTYPE_F32)
-    load8<STRATA_DTYPE_F32>(reinterpret_cast<const float*>(p) + i, v);
+    load_groups<STRATA_DTYPE_F32>(p, base, G, v);
   else if (dt == STRATA_DTYPE_F16)
-    load8<STRATA_DTYPE_F16>(reinterpret_cast<const uint16_t*>(p) + i, v);
+    load_groups<STRATA_DTYPE_F16>(p, base, G, v);
   else
-    load8<STRATA_DTYPE_BF16>(reinterpret_cast<const uint16_t*>(p) + i, v);
+    load_groups<STRATA_DTYPE_BF16>(p, base, G, v);
 }
 STRATA_DEVFN void store8_as(void* p, int dt, int64_t i, const float (&v)[8]) {
   if (dt == STRATA_DTYPE_F32)
@@ -46,24 +65,14 @@ __global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a
     const int64_t base = (int64_t)row * a.H;
     float r[VPT][8];
     float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int g = tid + nth * j;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[j][i] = 0.f;
-      if (g < G) load8_as(a.x, a.x_dtype, base + 8 * g, r[j]);
-    }
+load_groups_as<VPT>(a.x, a.x_dtype, base, G, r);
     if (a.delta) {
+      float d[VPT][8];
+      load_groups_as<VPT>(a.delta, a.delta_dtype, base, G, d);
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int g = tid + nth * j;
-        if (g < G) {
-          float d[8];
-          load8_as(a.delta, a.delta_dtype, base + 8 * g, d);
+      for (int j = 0; j < VPT; ++j)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r[j][i] += d[i];
-        }
-      }
+        for (int i = 0; i < 8; ++i) r[j][i] += d[j][i];
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -95,9 +104,9 @@ __global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a
         uint2 c;
         uint32_t e;
         if (a.fmt == STRATA_MX_FP4)
-          e = mx_encode8<STRATA_MX_FP4>(h, c);
+          e = mx_encode8<STRATA_MX_FP4>(h, max_bits8(h), c);
         else
-          e = mx_encode8<STRATA_MX_FP8>(h, c);
+          e = mx_encode8<STRATA_MX_FP8>(h, max_bits8(h), c);
         if (g < G) {
           if (a.fmt == STRATA_MX_FP4)
             reinterpret_cast<uint32_t*>(a.codes)[base / 8 + g] = c.x;

@@ -34,29 +34,46 @@ __host__ __device__ inline int64_t mx_tile_byte(int row, int block, int kt) {
 }
 
 // ---------------------------------------------------------------- 8 elements
-// Eight consecutive elements of a tensor of dtype DT at p (16-byte aligned).
+// Eight consecutive elements of a tensor of dtype DT (16-byte aligned), as
+// loaded.
 template <int DT>
-STRATA_DEVFN void load8(const void* p, float (&v)[8]) {
-  if constexpr (DT == STRATA_DTYPE_F32) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0];
-    const float4 b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw8 {
+  uint4 w[DT == STRATA_DTYPE_F32 ? 2 : 1];
+  STRATA_DEVFN void zero() {
+    for (uint4& q : w) q = make_uint4(0u, 0u, 0u, 0u);
+  }
+  STRATA_DEVFN void load(const void* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == STRATA_DTYPE_BF16) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        const float2 f = __half22float2(u32_as_h2(w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+    for (int i = 0; i < (int)(sizeof(w) / 16); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  STRATA_DEVFN void values(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(w) / 16); ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == STRATA_DTYPE_F32) {
+          v[4 * i + j] = __uint_as_float(u[j]);
+        } else if constexpr (DT == STRATA_DTYPE_BF16) {
+          v[2 * j] = __uint_as_float(u[j] << 16);
+          v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        } else {
+          const float2 f = __half22float2(u32_as_h2(u[j]));
+          v[2 * j] = f.x;
+          v[2 * j + 1] = f.y;
+        }
       }
     }
   }
+  // The largest magnitude as fp32 bits (16-bit types: two at a time as they
+  // are stored, whose bits order like the magnitudes too).
+  STRATA_DEVFN uint32_t max_bits(const float (&v)[8]) const;
+};
+template <int DT>
+STRATA_DEVFN void load8(const void* p, float (&v)[8]) {
+  Raw8<DT> r;
+  r.load(p);
+  r.values(v);
 }
 
 // Two values rounded to nearest even in the 16-bit type DT, first one low.
@@ -84,17 +101,15 @@ STRATA_DEVFN void store8(void* p, const float (&v)[8]) {
 
 // ---------------------------------------------------------------- one block
 // A block of 32 is held by four adjacent lanes, eight elements each; all 32
-// lanes of the warp call this.  Scale: floor(log2 m) is the exponent field of
-// the largest magnitude's bits (which order like the magnitudes, Inf and NaN
-// above every number), so e = field - emax, at least 0; subnormal m has field
-// 0 and lands on e = 0 as the clamp asks.  x * 2^(127-e) is exact but for
-// results below the smallest element, which round to zero either way.
+// lanes of the warp call this.  `m`: the largest of a lane's eight magnitudes
+// as fp32 bits, which order like the magnitudes, Inf and NaN above every
+// number.  floor(log2 m) is their exponent field, so e = field - emax, at
+// least 0; subnormal m has field 0 and lands on e = 0 as the clamp asks.
+// x * 2^(127-e) is exact but for results below the smallest element, which
+// round to zero either way.
 // Returns e; codes: FP4 in .x, FP8 in .x and .y.
 template <int FMT>
-STRATA_DEVFN uint32_t mx_encode8(const float (&v)[8], uint2& codes) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+STRATA_DEVFN uint32_t mx_encode8(const float (&v)[8], uint32_t m, uint2& codes) {
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   codes = make_uint2(0u, 0u);
@@ -116,6 +131,29 @@ STRATA_DEVFN uint32_t mx_encode8(const float (&v)[8], uint2& codes) {
     }
   }
   return (uint32_t)e;
+}
+STRATA_DEVFN uint32_t max_bits8(const float (&v)[8]) {
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(v[i]) & 0x7fffffffu;
+  return __vimax3_u32(__vimax3_u32(b[0], b[1], b[2]), __vimax3_u32(b[3], b[4], b[5]),
+                      max(b[6], b[7]));
+}
+
+template <int DT>
+STRATA_DEVFN uint32_t Raw8<DT>::max_bits(const float (&v)[8]) const {
+  if constexpr (DT == STRATA_DTYPE_F32) {
+    return max_bits8(v);
+  } else {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    const uint32_t m = __vimax3_u16x2(
+        __vimax3_u16x2(w[0].x & kAbs, w[0].y & kAbs, w[0].z & kAbs), w[0].w & kAbs, 0u);
+    const uint32_t h = max(m & 0xffffu, m >> 16);
+    if constexpr (DT == STRATA_DTYPE_BF16)
+      return h << 16;
+    else
+      return __float_as_uint(__half2float(__ushort_as_half((uint16_t)h))) & 0x7fffffffu;
+  }
 }
 
 // 2^(e-127) in fp32 (2^-127 is a subnormal; 255 is NaN).

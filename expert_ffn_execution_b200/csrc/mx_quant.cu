@@ -2,11 +2,13 @@
 // row order to the product's tiles.
 //
 // All three are one pass over their data: bound by HBM where that is large
-// and by the launch where it is small.  A thread takes 8 elements (one 16- or
-// two 16-byte loads), four lanes a block of 32; the block's scale comes from
-// two shuffles.  Four groups of 8 a thread are loaded before the first is
-// used.  Rows, matrices and padding are found from a flat group index whose
-// one 64-bit division is per CTA.
+// and by the launch where it is small.  A thread takes groups of 8 elements
+// (one 16- or two 16-byte loads), four lanes a block of 32; the block's scale
+// comes from two shuffles.  A thread loads its groups, kQThreads apart, before
+// it uses the first.  Matrix, row and column of the first come from its flat
+// index by division, those of the next by adding: with a division for each the
+// kernel was bound by instructions (36 us for 8192 x 4096 bf16 to FP8, 2.8
+// TB/s).
 #include "mx.cuh"
 #include "tc05.cuh"
 
@@ -17,98 +19,120 @@ namespace {
 constexpr int kQThreads = 256;
 constexpr int kQUnroll = 4;
 
-// Where group `i` (of 8 elements) of this CTA's kQThreads * kQUnroll lies:
-// rows of `per` groups, matrices of `rows_p` rows.
+// Matrix, row and group of 8 columns of a flat group index, for rows of `per`
+// groups and matrices of `rows` rows (padding included).
+struct Walk {
+  uint32_t per, rows;
+  uint32_t step_row, step_c;  // kQThreads = step_row * per + step_c
+  uint64_t total;
+};
+Walk make_walk(int64_t batch, int64_t rows, int64_t per) {
+  Walk w;
+  w.per = (uint32_t)per;
+  w.rows = (uint32_t)rows;
+  w.step_row = (uint32_t)(kQThreads / per);
+  w.step_c = (uint32_t)(kQThreads % per);
+  w.total = (uint64_t)(batch * rows * per);
+  return w;
+}
 struct Place {
   uint32_t batch, row, c;
 };
-STRATA_DEVFN Place place_of(uint64_t row0, uint32_t c0, uint32_t i, uint32_t per,
-                            uint32_t rows_p) {
-  const uint32_t l = c0 + i, dr = l / per;
-  const uint32_t r = (uint32_t)row0 + dr;
+STRATA_DEVFN Place first_place(const Walk& w, uint64_t g) {
   Place p;
-  p.c = l - dr * per;
-  p.batch = r / rows_p;
-  p.row = r - p.batch * rows_p;
+  uint32_t r;
+  if (w.total >> 32) {
+    r = (uint32_t)(g / w.per);
+    p.c = (uint32_t)(g - (uint64_t)r * w.per);
+  } else {
+    r = (uint32_t)g / w.per;
+    p.c = (uint32_t)g - r * w.per;
+  }
+  p.batch = r / w.rows;
+  p.row = r - p.batch * w.rows;
+  return p;
+}
+STRATA_DEVFN Place next_place(const Walk& w, Place p) {
+  p.c += w.step_c;
+  p.row += w.step_row;
+  if (p.c >= w.per) {
+    p.c -= w.per;
+    ++p.row;
+  }
+  while (p.row >= w.rows) {
+    p.row -= w.rows;
+    ++p.batch;
+  }
   return p;
 }
 
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(MxQuantArgs a, uint32_t per,
-                                                                uint32_t rows_p, uint64_t total) {
+__global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(MxQuantArgs a, Walk w) {
   constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
-  const uint64_t g0 = (uint64_t)blockIdx.x * (kQThreads * kQUnroll);
-  const uint64_t row0 = g0 / per;
-  const uint32_t c0 = (uint32_t)(g0 - row0 * per);
   const uint32_t groups = (uint32_t)(a.K / 8);
   const int kt = (int)mx_ceil(a.K, kMxTileBlocks * kMxBlock);
+  const int64_t row_bytes = mx_row_bytes(FMT, a.K);
   const uint8_t* src = reinterpret_cast<const uint8_t*>(a.src);
-  pdl_wait_prior();
-  float v[kQUnroll][8];
   Place p[kQUnroll];
-  bool in[kQUnroll], live[kQUnroll];
+  p[0] = first_place(w, (uint64_t)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x);
+#pragma unroll
+  for (int u = 1; u < kQUnroll; ++u) p[u] = next_place(w, p[u - 1]);
+  pdl_wait_prior();
+  Raw8<DT> raw[kQUnroll];
 #pragma unroll
   for (int u = 0; u < kQUnroll; ++u) {
-    const uint32_t i = u * kQThreads + threadIdx.x;
-    in[u] = g0 + i < total;
-    p[u] = place_of(row0, c0, i, per, rows_p);
-    live[u] = in[u] && p[u].row < (uint32_t)a.rows && p[u].c < groups;
-    if (live[u]) {
-      load8<DT>(src + ((int64_t)p[u].batch * a.batch_stride + (int64_t)p[u].row * a.row_stride +
-                       (int64_t)p[u].c * 8) * kEl,
-                v[u]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[u][j] = 0.f;  // padding of a scale tile: scale byte 0
-    }
+    if (p[u].batch < a.batch && p[u].row < a.rows && p[u].c < groups)
+      raw[u].load(src + ((int64_t)p[u].batch * a.batch_stride + (int64_t)p[u].row * a.row_stride +
+                         (int64_t)p[u].c * 8) * kEl);
+    else
+      raw[u].zero();  // padding of a scale tile: scale byte 0
   }
 #pragma unroll
   for (int u = 0; u < kQUnroll; ++u) {
+    float v[8];
+    raw[u].values(v);
     uint2 codes;
-    const uint32_t e = mx_encode8<FMT>(v[u], codes);
-    if (live[u]) {
-      uint8_t* o = a.codes + p[u].batch * a.codes_stride +
-                   (int64_t)p[u].row * mx_row_bytes(FMT, a.K) + mx_row_bytes(FMT, 8) * p[u].c;
+    const uint32_t e = mx_encode8<FMT>(v, raw[u].max_bits(v), codes);
+    if (p[u].batch >= a.batch) continue;
+    if (p[u].row < a.rows && p[u].c < groups) {
+      uint8_t* o = a.codes + p[u].batch * a.codes_stride + (int64_t)p[u].row * row_bytes +
+                   mx_row_bytes(FMT, 8) * p[u].c;
       if constexpr (FMT == STRATA_MX_FP4)
         *reinterpret_cast<uint32_t*>(o) = codes.x;
       else
         *reinterpret_cast<uint2*>(o) = codes;
     }
-    if (in[u] && (threadIdx.x & 3) == 0) {
+    if ((threadIdx.x & 3) == 0) {
       const int blk = (int)(p[u].c / 4);
       uint8_t* s = a.scales + p[u].batch * a.scales_stride;
       if (a.layout == STRATA_MX_TILES)
         s[mx_tile_byte((int)p[u].row, blk, kt)] = (uint8_t)e;
       else
-        s[(int64_t)p[u].row * (a.K / kMxBlock) + blk] = (uint8_t)e;
+        s[(int64_t)p[u].row * (groups / 4) + blk] = (uint8_t)e;
     }
   }
 }
 
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(MxDequantArgs a, uint32_t per,
-                                                                  uint64_t total) {
+__global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(MxDequantArgs a, Walk w) {
   constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
-  const uint64_t g0 = (uint64_t)blockIdx.x * (kQThreads * kQUnroll);
-  const uint64_t row0 = g0 / per;
-  const uint32_t c0 = (uint32_t)(g0 - row0 * per);
   const int kt = (int)mx_ceil(a.K, kMxTileBlocks * kMxBlock);
+  const int64_t row_bytes = mx_row_bytes(FMT, a.K);
   uint8_t* dst = reinterpret_cast<uint8_t*>(a.dst);
+  Place p[kQUnroll];
+  p[0] = first_place(w, (uint64_t)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x);
+#pragma unroll
+  for (int u = 1; u < kQUnroll; ++u) p[u] = next_place(w, p[u - 1]);
   pdl_wait_prior();
   uint2 codes[kQUnroll];
   uint32_t e[kQUnroll];
-  Place p[kQUnroll];
-  bool in[kQUnroll];
 #pragma unroll
   for (int u = 0; u < kQUnroll; ++u) {
-    const uint32_t i = u * kQThreads + threadIdx.x;
-    in[u] = g0 + i < total;
-    p[u] = place_of(row0, c0, i, per, (uint32_t)a.rows);
     codes[u] = make_uint2(0u, 0u);
     e[u] = 0;
-    if (in[u]) {
-      const uint8_t* c = a.codes + p[u].batch * a.codes_stride +
-                         (int64_t)p[u].row * mx_row_bytes(FMT, a.K) + mx_row_bytes(FMT, 8) * p[u].c;
+    if (p[u].batch < a.batch) {
+      const uint8_t* c = a.codes + p[u].batch * a.codes_stride + (int64_t)p[u].row * row_bytes +
+                         mx_row_bytes(FMT, 8) * p[u].c;
       if constexpr (FMT == STRATA_MX_FP4)
         codes[u].x = *reinterpret_cast<const uint32_t*>(c);
       else
@@ -116,12 +140,12 @@ __global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(MxDequantArgs 
       const int blk = (int)(p[u].c / 4);
       const uint8_t* s = a.scales + p[u].batch * a.scales_stride;
       e[u] = a.layout == STRATA_MX_TILES ? s[mx_tile_byte((int)p[u].row, blk, kt)]
-                                         : s[(int64_t)p[u].row * (a.K / kMxBlock) + blk];
+                                         : s[(int64_t)p[u].row * (w.per / 4) + blk];
     }
   }
 #pragma unroll
   for (int u = 0; u < kQUnroll; ++u) {
-    if (!in[u]) continue;
+    if (p[u].batch >= a.batch) continue;
     float v[8];
     mx_decode8<FMT>(codes[u], e[u], v);
     store8<DT>(dst + ((int64_t)p[u].batch * a.batch_stride + (int64_t)p[u].row * a.row_stride +
@@ -168,16 +192,14 @@ cudaError_t launch_groups(Kern kern, uint64_t total, uint64_t per_cta, cudaStrea
 }  // namespace
 
 cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t st) {
-  const bool tiles = a.layout == STRATA_MX_TILES;
   // with tiles, the padding rows and blocks of the scale tiles are visited too
-  const uint32_t per = (uint32_t)(tiles ? mx_ceil(a.K, 128) * 16 : a.K / 8);
-  const uint32_t rows_p =
-      (uint32_t)(tiles ? mx_ceil(a.rows, kMxTileRows) * kMxTileRows : a.rows);
-  const uint64_t total = (uint64_t)a.batch * rows_p * per;
+  const bool tiles = a.layout == STRATA_MX_TILES;
+  const Walk w = make_walk(a.batch, tiles ? mx_ceil(a.rows, kMxTileRows) * kMxTileRows : a.rows,
+                           tiles ? mx_ceil(a.K, 128) * 16 : a.K / 8);
   constexpr uint64_t cta = kQThreads * kQUnroll;
-#define STRATA_Q(DT, FMT)                                                                     \
-  if (a.src_dtype == DT && a.fmt == FMT)                                                      \
-    return launch_groups(mx_quantize_kernel<DT, FMT>, total, cta, st, a, per, rows_p, total);
+#define STRATA_Q(DT, FMT)                 \
+  if (a.src_dtype == DT && a.fmt == FMT)  \
+    return launch_groups(mx_quantize_kernel<DT, FMT>, w.total, cta, st, a, w);
   STRATA_Q(STRATA_DTYPE_F32, STRATA_MX_FP4)
   STRATA_Q(STRATA_DTYPE_F16, STRATA_MX_FP4)
   STRATA_Q(STRATA_DTYPE_BF16, STRATA_MX_FP4)
@@ -189,12 +211,11 @@ cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_mx_dequantize(const MxDequantArgs& a, cudaStream_t st) {
-  const uint32_t per = (uint32_t)(a.K / 8);
-  const uint64_t total = (uint64_t)a.batch * a.rows * per;
+  const Walk w = make_walk(a.batch, a.rows, a.K / 8);
   constexpr uint64_t cta = kQThreads * kQUnroll;
-#define STRATA_D(DT, FMT)                                                                \
-  if (a.dst_dtype == DT && a.fmt == FMT)                                                 \
-    return launch_groups(mx_dequantize_kernel<DT, FMT>, total, cta, st, a, per, total);
+#define STRATA_D(DT, FMT)                 \
+  if (a.dst_dtype == DT && a.fmt == FMT)  \
+    return launch_groups(mx_dequantize_kernel<DT, FMT>, w.total, cta, st, a, w);
   STRATA_D(STRATA_DTYPE_F32, STRATA_MX_FP4)
   STRATA_D(STRATA_DTYPE_F16, STRATA_MX_FP4)
   STRATA_D(STRATA_DTYPE_BF16, STRATA_MX_FP4)
