@@ -101,12 +101,19 @@ load_groups_as<VPT>(a.x, a.x_dtype, base, G, r);
       }
       if (a.out && g < G) store8_as(a.out, a.out_dtype, base + 8 * g, h);
       if (a.fmt) {
+        // four adjacent lanes hold a block of 32
+        uint32_t m = max_bits8(h);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         uint2 c;
         uint32_t e;
-        if (a.fmt == STRATA_MX_FP4)
-          e = mx_encode8<STRATA_MX_FP4>(h, max_bits8(h), c);
-        else
-          e = mx_encode8<STRATA_MX_FP8>(h, max_bits8(h), c);
+        if (a.fmt == STRATA_MX_FP4) {
+          e = mx_scale_of<STRATA_MX_FP4>(m);
+          c = mx_encode8<STRATA_MX_FP4>(h, e);
+        } else {
+          e = mx_scale_of<STRATA_MX_FP8>(m);
+          c = mx_encode8<STRATA_MX_FP8>(h, e);
+        }
         if (g < G) {
           if (a.fmt == STRATA_MX_FP4)
             reinterpret_cast<uint32_t*>(a.codes)[base / 8 + g] = c.x;

@@ -100,23 +100,23 @@ STRATA_DEVFN void store8(void* p, const float (&v)[8]) {
 }
 
 // ---------------------------------------------------------------- one block
-// A block of 32 is held by four adjacent lanes, eight elements each; all 32
-// lanes of the warp call this.  `m`: the largest of a lane's eight magnitudes
-// as fp32 bits, which order like the magnitudes, Inf and NaN above every
-// number.  floor(log2 m) is their exponent field, so e = field - emax, at
-// least 0; subnormal m has field 0 and lands on e = 0 as the clamp asks.
-// x * 2^(127-e) is exact but for results below the smallest element, which
-// round to zero either way.
-// Returns e; codes: FP4 in .x, FP8 in .x and .y.
+// The scale byte of a block from the largest of its magnitudes as fp32 bits,
+// which order like the magnitudes, Inf and NaN above every number.
+// floor(log2 m) is their exponent field, so e = field - emax, at least 0;
+// subnormal m has field 0 and lands on e = 0 as the clamp asks.  A block with
+// Inf or NaN is NaN.
 template <int FMT>
-STRATA_DEVFN uint32_t mx_encode8(const float (&v)[8], uint32_t m, uint2& codes) {
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  codes = make_uint2(0u, 0u);
-  if (m >= 0x7f800000u) return 255u;  // Inf or NaN in the block: the block is NaN
+STRATA_DEVFN uint32_t mx_scale_of(uint32_t m) {
   constexpr int kEmax = FMT == STRATA_MX_FP4 ? 2 : 8;
-  const int e = max((int)(m >> 23) - kEmax, 0);
-  const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+  return m >= 0x7f800000u ? 255u : (uint32_t)max((int)(m >> 23) - kEmax, 0);
+}
+// Eight codes under scale byte e: FP4 in .x, FP8 in .x and .y.  x * 2^(127-e)
+// is exact but for results below the smallest element, which round to zero
+// either way.
+template <int FMT>
+STRATA_DEVFN uint2 mx_encode8(const float (&v)[8], uint32_t e) {
+  uint2 codes = make_uint2(0u, 0u);
+  const float inv = __uint_as_float((254u - e) << 23);  // not used for e = 255
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 p = make_float2(v[2 * i] * inv, v[2 * i + 1] * inv);
@@ -130,7 +130,7 @@ STRATA_DEVFN uint32_t mx_encode8(const float (&v)[8], uint32_t m, uint2& codes) 
         codes.y |= c << (16 * (i - 2));
     }
   }
-  return (uint32_t)e;
+  return e == 255u ? make_uint2(0u, 0u) : codes;
 }
 STRATA_DEVFN uint32_t max_bits8(const float (&v)[8]) {
   uint32_t b[8];

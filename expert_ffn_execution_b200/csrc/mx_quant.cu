@@ -2,13 +2,14 @@
 // row order to the product's tiles.
 //
 // All three are one pass over their data: bound by HBM where that is large
-// and by the launch where it is small.  A thread takes groups of 8 elements
-// (one 16- or two 16-byte loads), four lanes a block of 32; the block's scale
-// comes from two shuffles.  A thread loads its groups, kQThreads apart, before
-// it uses the first.  Matrix, row and column of the first come from its flat
-// index by division, those of the next by adding: with a division for each the
-// kernel was bound by instructions (36 us for 8192 x 4096 bf16 to FP8, 2.8
-// TB/s).
+// and by the launch where it is small; in between, by instructions, so what is
+// not the conversion itself is kept small.  A thread takes 16 elements at a
+// time (half a block: one shuffle joins two lanes' largest magnitudes), and
+// loads its kQUnroll pieces, kQThreads apart, before it uses the first.
+// Matrix, row and column of the first come from its flat index by division,
+// those of the next, and their offsets, by adding.  8192 x 4096 bf16 to FP8:
+// 36 us with 8 elements and three divisions a piece, 24 us without the
+// divisions, 18 us with 16 elements and added offsets.
 #include "mx.cuh"
 #include "tc05.cuh"
 
@@ -17,10 +18,11 @@ namespace strata {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kQUnroll = 4;
+constexpr int kQUnroll = 2;
+constexpr int kQEl = 16;  // elements of a piece
 
-// Matrix, row and group of 8 columns of a flat group index, for rows of `per`
-// groups and matrices of `rows` rows (padding included).
+// A walk over the pieces of a batch of matrices, kQThreads at a step, for rows
+// of `per` pieces and matrices of `rows` rows (padding included).
 struct Walk {
   uint32_t per, rows;
   uint32_t step_row, step_c;  // kQThreads = step_row * per + step_c
@@ -35,10 +37,27 @@ Walk make_walk(int64_t batch, int64_t rows, int64_t per) {
   w.total = (uint64_t)(batch * rows * per);
   return w;
 }
+// An offset linear in matrix, row and piece: what a step, the end of a row
+// and the end of a matrix add.
+struct Stride {
+  int64_t batch, row, piece;
+  int64_t step, row_end, batch_end;
+};
+Stride make_stride(const Walk& w, int64_t batch, int64_t row, int64_t piece) {
+  Stride s;
+  s.batch = batch;
+  s.row = row;
+  s.piece = piece;
+  s.step = (int64_t)w.step_row * row + (int64_t)w.step_c * piece;
+  s.row_end = row - (int64_t)w.per * piece;
+  s.batch_end = batch - (int64_t)w.rows * row;
+  return s;
+}
 struct Place {
   uint32_t batch, row, c;
+  int64_t src, dst;  // offsets by the two strides
 };
-STRATA_DEVFN Place first_place(const Walk& w, uint64_t g) {
+STRATA_DEVFN Place first_place(const Walk& w, const Stride& src, const Stride& dst, uint64_t g) {
   Place p;
   uint32_t r;
   if (w.total >> 32) {
@@ -50,107 +69,127 @@ STRATA_DEVFN Place first_place(const Walk& w, uint64_t g) {
   }
   p.batch = r / w.rows;
   p.row = r - p.batch * w.rows;
+  p.src = p.batch * src.batch + p.row * src.row + p.c * src.piece;
+  p.dst = p.batch * dst.batch + p.row * dst.row + p.c * dst.piece;
   return p;
 }
-STRATA_DEVFN Place next_place(const Walk& w, Place p) {
+STRATA_DEVFN Place next_place(const Walk& w, const Stride& src, const Stride& dst, Place p) {
   p.c += w.step_c;
   p.row += w.step_row;
+  p.src += src.step;
+  p.dst += dst.step;
   if (p.c >= w.per) {
     p.c -= w.per;
     ++p.row;
+    p.src += src.row_end;
+    p.dst += dst.row_end;
   }
   while (p.row >= w.rows) {
     p.row -= w.rows;
     ++p.batch;
+    p.src += src.batch_end;
+    p.dst += dst.batch_end;
   }
   return p;
 }
+// The scale byte of a place's block.
+STRATA_DEVFN int64_t scale_at(const Place& p, int layout, uint64_t batch_stride, int64_t blocks,
+                              int kt) {
+  const int blk = (int)(p.c / 2);
+  return (int64_t)(p.batch * batch_stride) +
+         (layout == STRATA_MX_TILES ? mx_tile_byte((int)p.row, blk, kt) : p.row * blocks + blk);
+}
 
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(MxQuantArgs a, Walk w) {
-  constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
-  const uint32_t groups = (uint32_t)(a.K / 8);
+__global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(MxQuantArgs a, Walk w, Stride ss,
+                                                                Stride sd) {
+  const uint32_t pieces = (uint32_t)(a.K / kQEl);
   const int kt = (int)mx_ceil(a.K, kMxTileBlocks * kMxBlock);
-  const int64_t row_bytes = mx_row_bytes(FMT, a.K);
   const uint8_t* src = reinterpret_cast<const uint8_t*>(a.src);
   Place p[kQUnroll];
-  p[0] = first_place(w, (uint64_t)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x);
+  p[0] = first_place(w, ss, sd, (uint64_t)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x);
 #pragma unroll
-  for (int u = 1; u < kQUnroll; ++u) p[u] = next_place(w, p[u - 1]);
+  for (int u = 1; u < kQUnroll; ++u) p[u] = next_place(w, ss, sd, p[u - 1]);
   pdl_wait_prior();
-  Raw8<DT> raw[kQUnroll];
+  Raw8<DT> raw[kQUnroll][2];
 #pragma unroll
   for (int u = 0; u < kQUnroll; ++u) {
-    if (p[u].batch < a.batch && p[u].row < a.rows && p[u].c < groups)
-      raw[u].load(src + ((int64_t)p[u].batch * a.batch_stride + (int64_t)p[u].row * a.row_stride +
-                         (int64_t)p[u].c * 8) * kEl);
-    else
-      raw[u].zero();  // padding of a scale tile: scale byte 0
+    if (p[u].batch < a.batch && p[u].row < a.rows && p[u].c < pieces) {
+      raw[u][0].load(src + p[u].src);
+      raw[u][1].load(src + p[u].src + sizeof(raw[u][0]));
+    } else {  // padding of a scale tile: scale byte 0
+      raw[u][0].zero();
+      raw[u][1].zero();
+    }
   }
 #pragma unroll
   for (int u = 0; u < kQUnroll; ++u) {
-    float v[8];
-    raw[u].values(v);
-    uint2 codes;
-    const uint32_t e = mx_encode8<FMT>(v, raw[u].max_bits(v), codes);
+    float v0[8], v1[8];
+    raw[u][0].values(v0);
+    raw[u][1].values(v1);
+    uint32_t m = max(raw[u][0].max_bits(v0), raw[u][1].max_bits(v1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t e = mx_scale_of<FMT>(m);
     if (p[u].batch >= a.batch) continue;
-    if (p[u].row < a.rows && p[u].c < groups) {
-      uint8_t* o = a.codes + p[u].batch * a.codes_stride + (int64_t)p[u].row * row_bytes +
-                   mx_row_bytes(FMT, 8) * p[u].c;
+    if (p[u].row < a.rows && p[u].c < pieces) {
+      const uint2 c0 = mx_encode8<FMT>(v0, e), c1 = mx_encode8<FMT>(v1, e);
       if constexpr (FMT == STRATA_MX_FP4)
-        *reinterpret_cast<uint32_t*>(o) = codes.x;
+        *reinterpret_cast<uint2*>(a.codes + p[u].dst) = make_uint2(c0.x, c1.x);
       else
-        *reinterpret_cast<uint2*>(o) = codes;
+        *reinterpret_cast<uint4*>(a.codes + p[u].dst) = make_uint4(c0.x, c0.y, c1.x, c1.y);
     }
-    if ((threadIdx.x & 3) == 0) {
-      const int blk = (int)(p[u].c / 4);
-      uint8_t* s = a.scales + p[u].batch * a.scales_stride;
-      if (a.layout == STRATA_MX_TILES)
-        s[mx_tile_byte((int)p[u].row, blk, kt)] = (uint8_t)e;
-      else
-        s[(int64_t)p[u].row * (groups / 4) + blk] = (uint8_t)e;
-    }
+    if ((threadIdx.x & 1) == 0)
+      a.scales[scale_at(p[u], a.layout, a.scales_stride, pieces / 2, kt)] = (uint8_t)e;
   }
 }
 
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(MxDequantArgs a, Walk w) {
+__global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(MxDequantArgs a, Walk w,
+                                                                  Stride ss, Stride sd) {
   constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
   const int kt = (int)mx_ceil(a.K, kMxTileBlocks * kMxBlock);
-  const int64_t row_bytes = mx_row_bytes(FMT, a.K);
   uint8_t* dst = reinterpret_cast<uint8_t*>(a.dst);
   Place p[kQUnroll];
-  p[0] = first_place(w, (uint64_t)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x);
+  p[0] = first_place(w, ss, sd, (uint64_t)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x);
 #pragma unroll
-  for (int u = 1; u < kQUnroll; ++u) p[u] = next_place(w, p[u - 1]);
+  for (int u = 1; u < kQUnroll; ++u) p[u] = next_place(w, ss, sd, p[u - 1]);
   pdl_wait_prior();
-  uint2 codes[kQUnroll];
+  uint2 c0[kQUnroll], c1[kQUnroll];
   uint32_t e[kQUnroll];
 #pragma unroll
   for (int u = 0; u < kQUnroll; ++u) {
-    codes[u] = make_uint2(0u, 0u);
+    c0[u] = c1[u] = make_uint2(0u, 0u);
     e[u] = 0;
-    if (p[u].batch < a.batch) {
-      const uint8_t* c = a.codes + p[u].batch * a.codes_stride + (int64_t)p[u].row * row_bytes +
-                         mx_row_bytes(FMT, 8) * p[u].c;
-      if constexpr (FMT == STRATA_MX_FP4)
-        codes[u].x = *reinterpret_cast<const uint32_t*>(c);
-      else
-        codes[u] = *reinterpret_cast<const uint2*>(c);
-      const int blk = (int)(p[u].c / 4);
-      const uint8_t* s = a.scales + p[u].batch * a.scales_stride;
-      e[u] = a.layout == STRATA_MX_TILES ? s[mx_tile_byte((int)p[u].row, blk, kt)]
-                                         : s[(int64_t)p[u].row * (w.per / 4) + blk];
+    if (p[u].batch >= a.batch) continue;
+    if constexpr (FMT == STRATA_MX_FP4) {
+      const uint2 c = *reinterpret_cast<const uint2*>(a.codes + p[u].src);
+      c0[u] = make_uint2(c.x, 0u);
+      c1[u] = make_uint2(c.y, 0u);
+    } else {
+      const uint4 c = *reinterpret_cast<const uint4*>(a.codes + p[u].src);
+      c0[u] = make_uint2(c.x, c.y);
+      c1[u] = make_uint2(c.z, c.w);
     }
+    e[u] = a.scales[scale_at(p[u], a.layout, a.scales_stride, w.per / 2, kt)];
   }
+  // The two lanes of a block trade halves of their codes, so that both write
+  // the first lane's 16 elements side by side, then the second's: with 16
+  // elements a lane in turn every store left half of each 32-byte sector to
+  // the next (29 us for 52M MXFP4 values to bf16, against 21.4 us).
+  const bool odd = threadIdx.x & 1;
 #pragma unroll
   for (int u = 0; u < kQUnroll; ++u) {
+    const uint2 give = odd ? c0[u] : c1[u];
+    uint2 got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+    got.y = FMT == STRATA_MX_FP4 ? 0u : __shfl_xor_sync(0xffffffffu, give.y, 1);
     if (p[u].batch >= a.batch) continue;
+    uint8_t* at = dst + p[u].dst - (odd ? 8 * kEl : 0);
     float v[8];
-    mx_decode8<FMT>(codes[u], e[u], v);
-    store8<DT>(dst + ((int64_t)p[u].batch * a.batch_stride + (int64_t)p[u].row * a.row_stride +
-                      (int64_t)p[u].c * 8) * kEl,
-               v);
+    mx_decode8<FMT>(odd ? got : c0[u], e[u], v);
+    store8<DT>(at, v);
+    mx_decode8<FMT>(odd ? c1[u] : got, e[u], v);
+    store8<DT>(at + kQEl * kEl, v);
   }
 }
 
@@ -195,11 +234,15 @@ cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t st) {
   // with tiles, the padding rows and blocks of the scale tiles are visited too
   const bool tiles = a.layout == STRATA_MX_TILES;
   const Walk w = make_walk(a.batch, tiles ? mx_ceil(a.rows, kMxTileRows) * kMxTileRows : a.rows,
-                           tiles ? mx_ceil(a.K, 128) * 16 : a.K / 8);
+                           tiles ? mx_ceil(a.K, 128) * (128 / kQEl) : a.K / kQEl);
+  const int64_t el = a.src_dtype == STRATA_DTYPE_F32 ? 4 : 2;
+  const Stride ss = make_stride(w, a.batch_stride * el, a.row_stride * el, kQEl * el);
+  const Stride sd = make_stride(w, (int64_t)a.codes_stride, mx_row_bytes(a.fmt, a.K),
+                                mx_row_bytes(a.fmt, kQEl));
   constexpr uint64_t cta = kQThreads * kQUnroll;
 #define STRATA_Q(DT, FMT)                 \
   if (a.src_dtype == DT && a.fmt == FMT)  \
-    return launch_groups(mx_quantize_kernel<DT, FMT>, w.total, cta, st, a, w);
+    return launch_groups(mx_quantize_kernel<DT, FMT>, w.total, cta, st, a, w, ss, sd);
   STRATA_Q(STRATA_DTYPE_F32, STRATA_MX_FP4)
   STRATA_Q(STRATA_DTYPE_F16, STRATA_MX_FP4)
   STRATA_Q(STRATA_DTYPE_BF16, STRATA_MX_FP4)
@@ -211,11 +254,15 @@ cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_mx_dequantize(const MxDequantArgs& a, cudaStream_t st) {
-  const Walk w = make_walk(a.batch, a.rows, a.K / 8);
+  const Walk w = make_walk(a.batch, a.rows, a.K / kQEl);
+  const int64_t el = a.dst_dtype == STRATA_DTYPE_F32 ? 4 : 2;
+  const Stride ss = make_stride(w, (int64_t)a.codes_stride, mx_row_bytes(a.fmt, a.K),
+                                mx_row_bytes(a.fmt, kQEl));
+  const Stride sd = make_stride(w, a.batch_stride * el, a.row_stride * el, kQEl * el);
   constexpr uint64_t cta = kQThreads * kQUnroll;
 #define STRATA_D(DT, FMT)                 \
   if (a.dst_dtype == DT && a.fmt == FMT)  \
-    return launch_groups(mx_dequantize_kernel<DT, FMT>, w.total, cta, st, a, w);
+    return launch_groups(mx_dequantize_kernel<DT, FMT>, w.total, cta, st, a, w, ss, sd);
   STRATA_D(STRATA_DTYPE_F32, STRATA_MX_FP4)
   STRATA_D(STRATA_DTYPE_F16, STRATA_MX_FP4)
   STRATA_D(STRATA_DTYPE_BF16, STRATA_MX_FP4)
