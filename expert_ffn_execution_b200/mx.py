@@ -4,11 +4,16 @@ that device's current stream (or `stream`).  No arithmetic happens here.
 
 A tensor that is used on another stream than the one it was made on is the
 caller's to order and to keep alive, as with any asynchronous call.
+
+A decode step's kernels take a few microseconds, so the host's part of a call
+counts: the current stream is read as a raw handle, the codes and scales that
+a call makes share one allocation, and their tensors are made when they are
+asked for.
 """
 from __future__ import annotations
 
 import contextlib
-from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -16,24 +21,26 @@ from . import _binding as B
 from .layer import ExpertWeights
 
 _DTYPES = {torch.float32: B.DTYPE_F32, torch.float16: B.DTYPE_F16, torch.bfloat16: B.DTYPE_BF16}
+_SAME = contextlib.nullcontext()
 
 
 def _dtype(dtype) -> int:
-    if dtype not in _DTYPES:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise TypeError(f"dtype {dtype}: float32, float16 or bfloat16 is wanted")
-    return _DTYPES[dtype]
+    return dt
 
 
 def _device(*tensors):
-    """The one CUDA device of the tensors."""
+    """The one CUDA device of the tensors (None among them is passed over)."""
     dev = None
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("the tensors must be on a CUDA device")
         if dev is None:
             dev = t.device
+            if dev.type != "cuda":
+                raise ValueError("the tensors must be on a CUDA device")
         elif t.device != dev:
             raise ValueError(f"tensors on {dev} and on {t.device}")
     return dev
@@ -41,45 +48,18 @@ def _device(*tensors):
 
 def _on(dev):
     """Makes `dev` the current device for a call (nothing to do where it is)."""
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    return _SAME if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _row_bytes(fmt: int, K: int) -> int:
-    return K // 2 if fmt == B.MX_FP4 else K
+def _stream_of(stream, dev) -> int:
+    """A stream argument as a handle; None: the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-@dataclass
-class MXTensor:
-    """A microscaled matrix [rows, K] on the device: uint8 codes [rows, K/2]
-    (MX_FP4) or [rows, K] (MX_FP8) and uint8 scales, [rows, K/32] (MX_ROWS) or
-    the flat plane of tiles that mx_linear reads (MX_TILES)."""
-    codes: torch.Tensor
-    scales: torch.Tensor
-    fmt: int
-    rows: int
-    K: int
-    layout: int
-
-    def __post_init__(self):
-        if self.fmt not in (B.MX_FP4, B.MX_FP8) or self.layout not in (B.MX_ROWS, B.MX_TILES):
-            raise ValueError("fmt must be MX_FP4 or MX_FP8, layout MX_ROWS or MX_TILES")
-        if self.rows < 0 or self.K < 32 or self.K % 32:
-            raise ValueError("rows must be >= 0 and K a positive multiple of 32")
-        for t, n, what in ((self.codes, self.rows * _row_bytes(self.fmt, self.K), "codes"),
-                           (self.scales, _scale_bytes(self.rows, self.K, self.layout), "scales")):
-            if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n:
-                raise ValueError(f"{what} must be contiguous uint8 of {n} bytes")
-
-    def dequantize(self, dtype=torch.float32, stream=None) -> torch.Tensor:
-        """The matrix's values: [rows, K] of `dtype`."""
-        dt, dev = _dtype(dtype), _device(self.codes, self.scales)
-        with _on(dev):
-            out = torch.empty(self.rows, self.K, dtype=dtype, device=dev)
-            B.moe_mx_dequantize(self.codes, 0, self.scales, self.layout, 0, self.fmt, 1, self.rows,
-                                self.K, out, dt, self.K, 0, stream)
-        return out
+def _code_bytes(rows: int, fmt: int, K: int) -> int:
+    return rows * (K // 2 if fmt == B.MX_FP4 else K)
 
 
 def _scale_bytes(rows: int, K: int, layout: int) -> int:
@@ -88,35 +68,94 @@ def _scale_bytes(rows: int, K: int, layout: int) -> int:
     return rows * (K // 32)
 
 
-def _empty_mx(rows: int, K: int, fmt: int, layout: int, dev) -> MXTensor:
-    shape = (rows, K // 32) if layout == B.MX_ROWS else (_scale_bytes(rows, K, layout),)
-    return MXTensor(torch.empty(rows, _row_bytes(fmt, K), dtype=torch.uint8, device=dev),
-                    torch.empty(shape, dtype=torch.uint8, device=dev), fmt, rows, K, layout)
+def _check_format(fmt, rows, K, layout):
+    if fmt not in (B.MX_FP4, B.MX_FP8) or layout not in (B.MX_ROWS, B.MX_TILES):
+        raise ValueError("fmt must be MX_FP4 or MX_FP8, layout MX_ROWS or MX_TILES")
+    if rows < 0 or K < 32 or K % 32:
+        raise ValueError(f"rows = {rows}, K = {K}: rows >= 0 and K a positive multiple of 32 are wanted")
 
 
-def _rows_of(x: torch.Tensor, what: str) -> torch.Tensor:
-    """x as the library reads rows: elements contiguous, each row on a 16-byte
-    boundary.  Other strides are refused, not copied."""
-    if x.dim() != 2:
-        raise ValueError(f"{what} must be a matrix, got shape {tuple(x.shape)}")
-    el = x.element_size()
-    if x.numel() and ((x.shape[1] > 1 and x.stride(1) != 1) or x.data_ptr() % 16
-                      or (x.shape[0] > 1 and x.stride(0) * el % 16)):
-        raise ValueError(f"{what} must have contiguous rows that start on 16-byte boundaries")
-    return x
+class MXTensor:
+    """A microscaled matrix [rows, K] on the device: uint8 codes [rows, K/2]
+    (MX_FP4) or [rows, K] (MX_FP8) and uint8 scales, [rows, K/32] (MX_ROWS) or
+    the flat plane of tiles that mx_linear reads (MX_TILES)."""
+
+    __slots__ = ("fmt", "rows", "K", "layout", "device", "codes_ptr", "scales_ptr", "_codes",
+                 "_scales", "_both")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: int, rows: int, K: int,
+                 layout: int):
+        _check_format(fmt, rows, K, layout)
+        for t, n, what in ((codes, _code_bytes(rows, fmt, K), "codes"),
+                           (scales, _scale_bytes(rows, K, layout), "scales")):
+            if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n:
+                raise ValueError(f"{what} must be contiguous uint8 of {n} bytes")
+        self.device = codes.device
+        if scales.device != self.device:
+            raise ValueError(f"codes on {self.device} and scales on {scales.device}")
+        self.fmt, self.rows, self.K, self.layout = fmt, rows, K, layout
+        self._codes, self._scales, self._both = codes, scales, None
+        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+
+    @classmethod
+    def _empty(cls, fmt: int, rows: int, K: int, layout: int, dev) -> MXTensor:
+        """One to be written by a call: both planes in one allocation."""
+        _check_format(fmt, rows, K, layout)
+        q = cls.__new__(cls)
+        q.fmt, q.rows, q.K, q.layout, q.device = fmt, rows, K, layout, dev
+        at = (_code_bytes(rows, fmt, K) + 255) & ~255
+        both = torch.empty(at + _scale_bytes(rows, K, layout), dtype=torch.uint8, device=dev)
+        q._codes = q._scales = None
+        q._both = both
+        q.codes_ptr = both.data_ptr()
+        q.scales_ptr = q.codes_ptr + at
+        return q
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            n = _code_bytes(self.rows, self.fmt, self.K)
+            self._codes = self._both[:n].view(self.rows, _code_bytes(1, self.fmt, self.K))
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            n = _scale_bytes(self.rows, self.K, self.layout)
+            s = self._both[self.scales_ptr - self.codes_ptr:][:n]
+            self._scales = s.view(self.rows, self.K // 32) if self.layout == B.MX_ROWS else s
+        return self._scales
+
+    def dequantize(self, dtype=torch.float32, stream=None) -> torch.Tensor:
+        """The matrix's values: [rows, K] of `dtype`."""
+        dt, dev = _dtype(dtype), self.device
+        if dev.type != "cuda":
+            raise ValueError("the tensors must be on a CUDA device")
+        with _on(dev):
+            out = torch.empty(self.rows, self.K, dtype=dtype, device=dev)
+            B.moe_mx_dequantize(self.codes_ptr, 0, self.scales_ptr, self.layout, 0, self.fmt, 1,
+                                self.rows, self.K, out.data_ptr(), dt, self.K, 0,
+                                _stream_of(stream, dev))
+        return out
 
 
 def mx_quantize(x: torch.Tensor, fmt: int, layout: int = B.MX_TILES, stream=None) -> MXTensor:
-    """x [rows, K] (rows may be strided) in the microscaled format `fmt`."""
-    _rows_of(x, "x")
+    """x [rows, K] in the microscaled format `fmt`.  Rows may be further apart
+    than they are long; other strides are refused, not copied."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be a matrix, got shape {tuple(x.shape)}")
     rows, K = x.shape
+    stride, step = x.stride()
+    dt, ptr = _dtype(x.dtype), x.data_ptr()
+    if rows and (step != 1 or ptr % 16 or (rows > 1 and stride * x.element_size() % 16)):
+        raise ValueError("x must have contiguous rows that start on 16-byte boundaries")
     if K < 32 or K % 32:
         raise ValueError(f"K = {K}: a positive multiple of 32 is wanted")
-    dt, dev = _dtype(x.dtype), _device(x)
+    dev = _device(x)
     with _on(dev):
-        q = _empty_mx(rows, K, fmt, layout, dev)
-        B.moe_mx_quantize(x, dt, 1, rows, K, x.stride(0), 0, fmt, q.codes, 0, q.scales, layout, 0,
-                          stream)
+        q = MXTensor._empty(fmt, rows, K, layout, dev)
+        B.moe_mx_quantize(ptr, dt, 1, rows, K, stride, 0, fmt, q.codes_ptr, 0, q.scales_ptr,
+                          layout, 0, _stream_of(stream, dev))
     return q
 
 
@@ -124,18 +163,17 @@ def mx_tile_scales(q: MXTensor, stream=None) -> MXTensor:
     """The same matrix with its scales in tiles, as mx_linear reads them."""
     if q.layout == B.MX_TILES:
         return q
-    dev = _device(q.codes, q.scales)
+    dev = _device(q.codes)
     with _on(dev):
         tiles = torch.empty(_scale_bytes(q.rows, q.K, B.MX_TILES), dtype=torch.uint8, device=dev)
-        B.moe_mx_tile_scales(q.scales, q.rows, q.K, tiles, stream)
+        B.moe_mx_tile_scales(q.scales_ptr, q.rows, q.K, tiles, _stream_of(stream, dev))
     return MXTensor(q.codes, tiles, q.fmt, q.rows, q.K, B.MX_TILES)
 
 
-@dataclass
-class AddNorm:
+class AddNorm(NamedTuple):
     """What add_rmsnorm gives: the new residual stream (x itself where there
-    was nothing to add), the normalised rows in 16 or 32 bits and in the
-    microscaled format, each None where it was not asked for."""
+    was nothing to add and no residual_out), the normalised rows in 16 or 32
+    bits and in the microscaled format, each None where it was not asked for."""
     residual: torch.Tensor
     out: torch.Tensor | None
     mx: MXTensor | None
@@ -148,9 +186,10 @@ def add_rmsnorm(x: torch.Tensor, delta: torch.Tensor | None = None,
     """r = x + delta; h = r / sqrt(mean r^2 + eps) * gain, per row of x [T, H];
     h as out_dtype (None: not written) and as microscaled `fmt` (0: not
     written).  r goes to residual_out (x for in place) or a new tensor."""
-    T, H = x.shape
+    shape = x.shape
+    T, H = shape
     for t, what in ((x, "x"), (delta, "delta"), (residual_out, "residual_out")):
-        if t is not None and (t.shape != x.shape or not t.is_contiguous()):
+        if t is not None and (t.shape != shape or not t.is_contiguous()):
             raise ValueError(f"{what} must be contiguous [T, H]")
     if residual_out is not None and residual_out.dtype != x.dtype:
         raise TypeError("residual_out must have the dtype of x")
@@ -159,17 +198,18 @@ def add_rmsnorm(x: torch.Tensor, delta: torch.Tensor | None = None,
         raise ValueError("gain must be contiguous float32 [H]")
     if out_dtype is None and not fmt:
         raise ValueError("ask for out_dtype, fmt or both")
-    dev = _device(x, delta, gain, residual_out)
     xd, dd = _dtype(x.dtype), 0 if delta is None else _dtype(delta.dtype)
     od = 0 if out_dtype is None else _dtype(out_dtype)
+    dev = _device(x, delta, gain, residual_out)
     with _on(dev):
         res = residual_out
         if res is None and delta is not None:
             res = torch.empty_like(x)
         out = None if out_dtype is None else torch.empty(T, H, dtype=out_dtype, device=dev)
-        q = _empty_mx(T, H, fmt, layout, dev) if fmt else None
+        q = MXTensor._empty(fmt, T, H, layout, dev) if fmt else None
         B.moe_add_rmsnorm(x, xd, delta, dd, gain, T, H, eps, res, out, od, fmt,
-                          q and q.codes, q and q.scales, layout, stream)
+                          None if q is None else q.codes_ptr, None if q is None else q.scales_ptr,
+                          layout, _stream_of(stream, dev))
     return AddNorm(x if res is None else res, out, q)
 
 
@@ -178,28 +218,31 @@ def mx_linear(x: MXTensor, w: MXTensor, bias: torch.Tensor | None = None,
               dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """x [T, K] times w [N, K] transposed, plus bias [N]: [T, N] of out_dtype
     (or of `out`, whose rows may be further apart than N)."""
-    if x.K != w.K:
-        raise ValueError(f"x has K = {x.K}, w K = {w.K}")
+    T, N, K = x.rows, w.rows, w.K
+    if x.K != K:
+        raise ValueError(f"x has K = {x.K}, w K = {K}")
     if x.layout != B.MX_TILES or w.layout != B.MX_TILES:
         raise ValueError("mx_linear reads scales in tiles: see mx_tile_scales")
-    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (w.rows,)
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (N,)
                              or not bias.is_contiguous()):
         raise ValueError("bias must be contiguous float32 [N]")
     if dev_status is not None and (dev_status.dtype != torch.int32 or not dev_status.numel()):
         raise ValueError("dev_status must be an int32 tensor")
+    ldy = N
     if out is not None:
-        if out.shape != (x.rows, w.rows) or (w.rows > 1 and out.stride(1) != 1) or \
-                (x.rows > 1 and out.stride(0) < w.rows):
+        if out.shape != (T, N) or (N > 1 and out.stride(1) != 1) or \
+                (T > 1 and out.stride(0) < N):
             raise ValueError("out must be [T, N] with contiguous rows that do not overlap")
         out_dtype = out.dtype
+        if T > 1:
+            ldy = out.stride(0)
     dt = _dtype(out_dtype)
-    dev = _device(x.codes, x.scales, w.codes, w.scales, bias, out, dev_status)
+    dev = _device(x, w, bias, out, dev_status)
     with _on(dev):
         if out is None:
-            out = torch.empty(x.rows, w.rows, dtype=out_dtype, device=dev)
-        ldy = out.stride(0) if x.rows > 1 else w.rows
-        B.moe_mx_linear(x.codes, x.fmt, x.scales, x.rows, w.codes, w.fmt, w.scales, w.rows, w.K,
-                        bias, out, dt, ldy, dev_status, stream)
+            out = torch.empty(T, N, dtype=out_dtype, device=dev)
+        B.moe_mx_linear(x.codes_ptr, x.fmt, x.scales_ptr, T, w.codes_ptr, w.fmt, w.scales_ptr, N,
+                        K, bias, out, dt, ldy, dev_status, _stream_of(stream, dev))
     return out
 
 
@@ -230,13 +273,14 @@ def pack_experts(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
                 w.data_ptr() % 16:
             raise ValueError("weights must have contiguous rows that start on 16-byte boundaries")
     dts, dev = [_dtype(w.dtype) for w in ws], _device(*ws)
+    stream = _stream_of(stream, dev)
     stride = B.strata_expert_bytes(B.FMT_MXFP4_32, H, I)
     with _on(dev):
         blobs = torch.empty(E, stride, dtype=torch.uint8, device=dev)
+        at = blobs.data_ptr()
         for w, dt, (c, s, rows, K) in zip(ws, dts, _blob_planes(H, I)):
-            B.moe_mx_quantize(w, dt, E, rows, K, w.stride(1), w.stride(0), B.MX_FP4,
-                              blobs.data_ptr() + c, stride, blobs.data_ptr() + s, B.MX_ROWS,
-                              stride, stream)
+            B.moe_mx_quantize(w, dt, E, rows, K, w.stride(1), w.stride(0), B.MX_FP4, at + c,
+                              stride, at + s, B.MX_ROWS, stride, stream)
     return ExpertWeights(blobs, B.FMT_MXFP4_32, H, I)
 
 
@@ -245,12 +289,12 @@ def unpack_experts(w: ExpertWeights, dtype=torch.float32, stream=None):
     if w.fmt != B.FMT_MXFP4_32:
         raise ValueError("only MXFP4 blobs are read back")
     dt, dev, E = _dtype(dtype), _device(w.blobs), w.num_experts
+    stream, at, stride = _stream_of(stream, dev), w.blobs.data_ptr(), w.blobs.stride(0)
     with _on(dev):
         outs = []
         for c, s, rows, K in _blob_planes(w.hidden, w.inter):
             o = torch.empty(E, rows, K, dtype=dtype, device=dev)
-            B.moe_mx_dequantize(w.blobs.data_ptr() + c, w.blobs.stride(0), w.blobs.data_ptr() + s,
-                                B.MX_ROWS, w.blobs.stride(0), B.MX_FP4, E, rows, K, o, dt, K,
-                                rows * K, stream)
+            B.moe_mx_dequantize(at + c, stride, at + s, B.MX_ROWS, stride, B.MX_FP4, E, rows, K, o,
+                                dt, K, rows * K, stream)
             outs.append(o)
     return tuple(outs)
