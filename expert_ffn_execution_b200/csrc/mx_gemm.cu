@@ -47,7 +47,7 @@ struct GemmCfg {
   static_assert(kGN + S * sfcols <= 512, "sums and scales fit the tensor memory");
 };
 
-template <int XF, int WF>
+template <int XF, int WF, int DT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                const __grid_constant__ CUtensorMap xsmap, const __grid_constant__ CUtensorMap wsmap,
@@ -89,7 +89,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers and tensor memory are ready
+  cluster_sync_relaxed();  // both CTAs' barriers and tensor memory are ready
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   pdl_wait_prior();
@@ -173,7 +173,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     const int q = warp % 4, half = warp / 4;
     uint8_t* buf = epi + warp * (32 * 64);
     const uint32_t lead = cluster_addr(smem_addr(tempty), 0);
-    const int el = a.y_dtype == STRATA_DTYPE_F32 ? 4 : 2;
+    constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
+    constexpr int kPer = 64 / kEl;   // features a pass
     int it = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++it) {
       const int t0 = (tile % mt) * kGM + 128 * (int)rank + 32 * q;
@@ -189,65 +190,53 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(lead);
+      if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (n0 + i < a.N) r[i] = __float_as_uint(__uint_as_float(r[i]) + a.bias[n0 + i]);
+      }
+      if constexpr (kEl == 2) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          r[i] = pack2<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      }
       // 64 bytes of each of the 32 rows at a time through shared memory, the
       // 16-byte pieces of row r at places piece ^ (r/2 % 4): both the writes
       // (a row a lane) and the reads (four lanes a row) touch every bank once
       const int rows = min(32, a.T - t0);
-      const int per = 64 / el;  // features a pass
+      uint8_t* const yb = reinterpret_cast<uint8_t*>(a.y) + ((int64_t)t0 * a.ldy + n0) * kEl;
+      const bool whole = vec && n0 + 128 <= a.N && rows > 0;
+      const int row = lane / 4, pc = lane % 4;
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        if (p * per >= 128) break;
-        const int nb = n0 + p * per;
-        if (nb >= a.N || rows <= 0) break;
-        uint32_t w[16];
-        if (el == 4) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float v = __uint_as_float(r[(16 * p + i) & 127]);
-            if (a.bias) v += nb + i < a.N ? a.bias[nb + i] : 0.f;
-            w[i] = __float_as_uint(v);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float v0 = __uint_as_float(r[(32 * p + 2 * i) & 127]);
-            float v1 = __uint_as_float(r[(32 * p + 2 * i + 1) & 127]);
-            if (a.bias) {
-              v0 += nb + 2 * i < a.N ? a.bias[nb + 2 * i] : 0.f;
-              v1 += nb + 2 * i + 1 < a.N ? a.bias[nb + 2 * i + 1] : 0.f;
-            }
-            w[i] = a.y_dtype == STRATA_DTYPE_F16 ? pack2<STRATA_DTYPE_F16>(v0, v1)
-                                                 : pack2<STRATA_DTYPE_BF16>(v0, v1);
-          }
-        }
+      for (int p = 0; p < 128 / kPer; ++p) {
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ (lane / 2)) & 3) * 16) =
-              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              make_uint4(r[16 * p + 4 * i], r[16 * p + 4 * i + 1], r[16 * p + 4 * i + 2],
+                         r[16 * p + 4 * i + 3]);
         __syncwarp();
-        uint8_t* yb = reinterpret_cast<uint8_t*>(a.y) + ((int64_t)t0 * a.ldy + nb) * el;
-        if (vec && nb + per <= a.N) {
+        if (whole) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int row = g * 8 + lane / 4, pc = lane % 4;
-            if (row < rows)
-              *reinterpret_cast<uint4*>(yb + (int64_t)row * a.ldy * el + pc * 16) =
-                  *reinterpret_cast<const uint4*>(buf + row * 64 + ((pc ^ (row / 2)) & 3) * 16);
-          }
+          for (int g = 0; g < 4; ++g)
+            if (g * 8 + row < rows)
+              *reinterpret_cast<uint4*>(yb + (int64_t)(g * 8 + row) * a.ldy * kEl + p * 64 +
+                                        pc * 16) =
+                  *reinterpret_cast<const uint4*>(buf + (g * 8 + row) * 64 +
+                                                  ((pc ^ (row / 2)) & 3) * 16);
         } else {
-          // rows without 16-byte boundaries, or the last features
-          const int left = min(per, a.N - nb);
-          for (int row = 0; row < rows; ++row) {
+          // rows without 16-byte boundaries, or the last features: a lane a feature
+          const int left = min(kPer, a.N - n0 - p * kPer);
+#pragma unroll 1
+          for (int w = 0; w < rows; ++w) {
             if (lane >= left) continue;
-            const int at = lane * el;
-            const uint8_t* src = buf + row * 64 + (((at / 16) ^ (row / 2)) & 3) * 16 + at % 16;
-            if (el == 4)
-              *reinterpret_cast<uint32_t*>(yb + (int64_t)row * a.ldy * 4 + at) =
-                  *reinterpret_cast<const uint32_t*>(src);
+            const int at = lane * kEl;
+            const uint8_t* src = buf + w * 64 + (((at / 16) ^ (w / 2)) & 3) * 16 + at % 16;
+            uint8_t* dst = yb + (int64_t)w * a.ldy * kEl + p * 64 + at;
+            if constexpr (kEl == 4)
+              *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
             else
-              *reinterpret_cast<uint16_t*>(yb + (int64_t)row * a.ldy * 2 + at) =
-                  *reinterpret_cast<const uint16_t*>(src);
+              *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
           }
         }
       }
@@ -265,7 +254,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     }
   }
   __syncthreads();
-  cluster_sync_all();
+  cluster_sync_relaxed();
   if (warp == kGEpi + 1) {
     tc_fence_after();
     tmem_dealloc_pair(tbase, 512);
@@ -293,7 +282,7 @@ bool make_scale_map(CUtensorMap* map, const uint8_t* scales, int rows, int K, in
                    CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <int XF, int WF>
+template <int XF, int WF, int DT>
 cudaError_t launch_gemm(const MxLinearArgs& a, cudaStream_t st) {
   using C = GemmCfg<XF, WF>;
   CUtensorMap xmap, wmap, xsmap, wsmap;
@@ -304,9 +293,9 @@ cudaError_t launch_gemm(const MxLinearArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int mt = (a.T + kGM - 1) / kGM, nt = (a.N + kGN - 1) / kGN;
   const int tiles = mt * nt;
-  const int el = a.y_dtype == STRATA_DTYPE_F32 ? 4 : 2;
+  constexpr int el = DT == STRATA_DTYPE_F32 ? 4 : 2;
   const int vec = (reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy * el % 16 == 0) ? 1 : 0;
-  auto kern = mx_gemm_kernel<XF, WF>;
+  auto kern = mx_gemm_kernel<XF, WF, DT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -322,12 +311,19 @@ cudaError_t launch_gemm(const MxLinearArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, xmap, wmap, xsmap, wsmap, a, mt, tiles, vec);
 }
 
+template <int XF, int WF>
+cudaError_t launch_gemm_y(const MxLinearArgs& a, cudaStream_t st) {
+  if (a.y_dtype == STRATA_DTYPE_F32) return launch_gemm<XF, WF, STRATA_DTYPE_F32>(a, st);
+  if (a.y_dtype == STRATA_DTYPE_F16) return launch_gemm<XF, WF, STRATA_DTYPE_F16>(a, st);
+  return launch_gemm<XF, WF, STRATA_DTYPE_BF16>(a, st);
+}
+
 }  // namespace
 
 cudaError_t launch_mx_gemm(const MxLinearArgs& a, cudaStream_t st) {
-  if (a.x_fmt == STRATA_MX_FP4) return launch_gemm<STRATA_MX_FP4, STRATA_MX_FP4>(a, st);
-  if (a.w_fmt == STRATA_MX_FP4) return launch_gemm<STRATA_MX_FP8, STRATA_MX_FP4>(a, st);
-  return launch_gemm<STRATA_MX_FP8, STRATA_MX_FP8>(a, st);
+  if (a.x_fmt == STRATA_MX_FP4) return launch_gemm_y<STRATA_MX_FP4, STRATA_MX_FP4>(a, st);
+  if (a.w_fmt == STRATA_MX_FP4) return launch_gemm_y<STRATA_MX_FP8, STRATA_MX_FP4>(a, st);
+  return launch_gemm_y<STRATA_MX_FP8, STRATA_MX_FP8>(a, st);
 }
 
 }  // namespace strata

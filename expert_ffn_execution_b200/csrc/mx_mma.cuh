@@ -162,20 +162,23 @@ STRATA_DEVFN void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without ordering memory: for barriers made visible by their own
+// fence, and for shared memory that only has to stay allocated.  (The release
+// above waits for the CTA's outstanding global writes: 0.5 us and more.)
+STRATA_DEVFN void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 STRATA_DEVFN uint32_t cluster_ctarank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-STRATA_DEVFN float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n\t.reg .b32 ra;\n\t"
-      "mapa.shared::cluster.u32 ra, %1, %2;\n\t"
-      "ld.shared::cluster.f32 %0, [ra];\n\t}"
-      : "=f"(v)
-      : "r"(saddr), "r"(rank)
-      : "memory");
+STRATA_DEVFN float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
   return v;
 }
 
