@@ -6,13 +6,12 @@ A tensor that is used on another stream than the one it was made on is the
 caller's to order and to keep alive, as with any asynchronous call.
 
 A decode step's kernels take a few microseconds, so the host's part of a call
-counts: the current stream is read as a raw handle, the codes and scales that
-a call makes share one allocation, and their tensors are made when they are
-asked for.
+counts: the library's functions are called directly, the current stream is
+read as a raw handle, the codes and scales that a call makes share one
+allocation, and their tensors are made when they are asked for.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple
 
 import torch
@@ -21,7 +20,6 @@ from . import _binding as B
 from .layer import ExpertWeights
 
 _DTYPES = {torch.float32: B.DTYPE_F32, torch.float16: B.DTYPE_F16, torch.bfloat16: B.DTYPE_BF16}
-_SAME = contextlib.nullcontext()
 
 
 def _dtype(dtype) -> int:
@@ -31,31 +29,35 @@ def _dtype(dtype) -> int:
     return dt
 
 
-def _device(*tensors):
-    """The one CUDA device of the tensors (None among them is passed over)."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-            if dev.type != "cuda":
-                raise ValueError("the tensors must be on a CUDA device")
-        elif t.device != dev:
+def _device(first, *others):
+    """The one CUDA device of the tensors (None among the others is passed over)."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    for t in others:
+        if t is not None and t.device != dev:
             raise ValueError(f"tensors on {dev} and on {t.device}")
     return dev
 
 
-def _on(dev):
-    """Makes `dev` the current device for a call (nothing to do where it is)."""
-    return _SAME if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _stream_of(stream, dev) -> int:
-    """A stream argument as a handle; None: the device's current stream."""
+def _call(name, dev, stream, *args):
+    """The library's `name` on `dev`, on `stream` (None: its current stream)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    fn = getattr(B._lib or B.load(), name)
+    if dev.index == torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc:
+        raise B.StrataError(name, rc)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _code_bytes(rows: int, fmt: int, K: int) -> int:
@@ -104,10 +106,9 @@ class MXTensor:
         q = cls.__new__(cls)
         q.fmt, q.rows, q.K, q.layout, q.device = fmt, rows, K, layout, dev
         at = (_code_bytes(rows, fmt, K) + 255) & ~255
-        both = torch.empty(at + _scale_bytes(rows, K, layout), dtype=torch.uint8, device=dev)
+        q._both = torch.empty(at + _scale_bytes(rows, K, layout), dtype=torch.uint8, device=dev)
         q._codes = q._scales = None
-        q._both = both
-        q.codes_ptr = both.data_ptr()
+        q.codes_ptr = q._both.data_ptr()
         q.scales_ptr = q.codes_ptr + at
         return q
 
@@ -128,14 +129,10 @@ class MXTensor:
 
     def dequantize(self, dtype=torch.float32, stream=None) -> torch.Tensor:
         """The matrix's values: [rows, K] of `dtype`."""
-        dt, dev = _dtype(dtype), self.device
-        if dev.type != "cuda":
-            raise ValueError("the tensors must be on a CUDA device")
-        with _on(dev):
-            out = torch.empty(self.rows, self.K, dtype=dtype, device=dev)
-            B.moe_mx_dequantize(self.codes_ptr, 0, self.scales_ptr, self.layout, 0, self.fmt, 1,
-                                self.rows, self.K, out.data_ptr(), dt, self.K, 0,
-                                _stream_of(stream, dev))
+        dt, dev = _dtype(dtype), _device(self)
+        out = torch.empty(self.rows, self.K, dtype=dtype, device=dev)
+        _call("moe_mx_dequantize", dev, stream, self.codes_ptr, 0, self.scales_ptr, self.layout, 0,
+              self.fmt, 1, self.rows, self.K, out.data_ptr(), dt, self.K, 0)
         return out
 
 
@@ -152,10 +149,9 @@ def mx_quantize(x: torch.Tensor, fmt: int, layout: int = B.MX_TILES, stream=None
     if K < 32 or K % 32:
         raise ValueError(f"K = {K}: a positive multiple of 32 is wanted")
     dev = _device(x)
-    with _on(dev):
-        q = MXTensor._empty(fmt, rows, K, layout, dev)
-        B.moe_mx_quantize(ptr, dt, 1, rows, K, stride, 0, fmt, q.codes_ptr, 0, q.scales_ptr,
-                          layout, 0, _stream_of(stream, dev))
+    q = MXTensor._empty(fmt, rows, K, layout, dev)
+    _call("moe_mx_quantize", dev, stream, ptr, dt, 1, rows, K, stride, 0, fmt, q.codes_ptr, 0,
+          q.scales_ptr, layout, 0)
     return q
 
 
@@ -163,10 +159,9 @@ def mx_tile_scales(q: MXTensor, stream=None) -> MXTensor:
     """The same matrix with its scales in tiles, as mx_linear reads them."""
     if q.layout == B.MX_TILES:
         return q
-    dev = _device(q.codes)
-    with _on(dev):
-        tiles = torch.empty(_scale_bytes(q.rows, q.K, B.MX_TILES), dtype=torch.uint8, device=dev)
-        B.moe_mx_tile_scales(q.scales_ptr, q.rows, q.K, tiles, _stream_of(stream, dev))
+    dev = _device(q)
+    tiles = torch.empty(_scale_bytes(q.rows, q.K, B.MX_TILES), dtype=torch.uint8, device=dev)
+    _call("moe_mx_tile_scales", dev, stream, q.scales_ptr, q.rows, q.K, tiles.data_ptr())
     return MXTensor(q.codes, tiles, q.fmt, q.rows, q.K, B.MX_TILES)
 
 
@@ -201,15 +196,14 @@ def add_rmsnorm(x: torch.Tensor, delta: torch.Tensor | None = None,
     xd, dd = _dtype(x.dtype), 0 if delta is None else _dtype(delta.dtype)
     od = 0 if out_dtype is None else _dtype(out_dtype)
     dev = _device(x, delta, gain, residual_out)
-    with _on(dev):
-        res = residual_out
-        if res is None and delta is not None:
-            res = torch.empty_like(x)
-        out = None if out_dtype is None else torch.empty(T, H, dtype=out_dtype, device=dev)
-        q = MXTensor._empty(fmt, T, H, layout, dev) if fmt else None
-        B.moe_add_rmsnorm(x, xd, delta, dd, gain, T, H, eps, res, out, od, fmt,
-                          None if q is None else q.codes_ptr, None if q is None else q.scales_ptr,
-                          layout, _stream_of(stream, dev))
+    res = residual_out
+    if res is None and delta is not None:
+        res = torch.empty_like(x)
+    out = None if out_dtype is None else torch.empty(T, H, dtype=out_dtype, device=dev)
+    q = MXTensor._empty(fmt, T, H, layout, dev) if fmt else None
+    _call("moe_add_rmsnorm", dev, stream, x.data_ptr(), xd, _ptr(delta), dd, _ptr(gain), T, H, eps,
+          _ptr(res), _ptr(out), od, fmt, q.codes_ptr if fmt else None,
+          q.scales_ptr if fmt else None, layout)
     return AddNorm(x if res is None else res, out, q)
 
 
@@ -238,11 +232,10 @@ def mx_linear(x: MXTensor, w: MXTensor, bias: torch.Tensor | None = None,
             ldy = out.stride(0)
     dt = _dtype(out_dtype)
     dev = _device(x, w, bias, out, dev_status)
-    with _on(dev):
-        if out is None:
-            out = torch.empty(T, N, dtype=out_dtype, device=dev)
-        B.moe_mx_linear(x.codes_ptr, x.fmt, x.scales_ptr, T, w.codes_ptr, w.fmt, w.scales_ptr, N,
-                        K, bias, out, dt, ldy, dev_status, _stream_of(stream, dev))
+    if out is None:
+        out = torch.empty(T, N, dtype=out_dtype, device=dev)
+    _call("moe_mx_linear", dev, stream, x.codes_ptr, x.fmt, x.scales_ptr, T, w.codes_ptr, w.fmt,
+          w.scales_ptr, N, K, _ptr(bias), out.data_ptr(), dt, ldy, _ptr(dev_status))
     return out
 
 
@@ -273,14 +266,12 @@ def pack_experts(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
                 w.data_ptr() % 16:
             raise ValueError("weights must have contiguous rows that start on 16-byte boundaries")
     dts, dev = [_dtype(w.dtype) for w in ws], _device(*ws)
-    stream = _stream_of(stream, dev)
     stride = B.strata_expert_bytes(B.FMT_MXFP4_32, H, I)
-    with _on(dev):
-        blobs = torch.empty(E, stride, dtype=torch.uint8, device=dev)
-        at = blobs.data_ptr()
-        for w, dt, (c, s, rows, K) in zip(ws, dts, _blob_planes(H, I)):
-            B.moe_mx_quantize(w, dt, E, rows, K, w.stride(1), w.stride(0), B.MX_FP4, at + c,
-                              stride, at + s, B.MX_ROWS, stride, stream)
+    blobs = torch.empty(E, stride, dtype=torch.uint8, device=dev)
+    at = blobs.data_ptr()
+    for w, dt, (c, s, rows, K) in zip(ws, dts, _blob_planes(H, I)):
+        _call("moe_mx_quantize", dev, stream, w.data_ptr(), dt, E, rows, K, w.stride(1),
+              w.stride(0), B.MX_FP4, at + c, stride, at + s, B.MX_ROWS, stride)
     return ExpertWeights(blobs, B.FMT_MXFP4_32, H, I)
 
 
@@ -289,12 +280,11 @@ def unpack_experts(w: ExpertWeights, dtype=torch.float32, stream=None):
     if w.fmt != B.FMT_MXFP4_32:
         raise ValueError("only MXFP4 blobs are read back")
     dt, dev, E = _dtype(dtype), _device(w.blobs), w.num_experts
-    stream, at, stride = _stream_of(stream, dev), w.blobs.data_ptr(), w.blobs.stride(0)
-    with _on(dev):
-        outs = []
-        for c, s, rows, K in _blob_planes(w.hidden, w.inter):
-            o = torch.empty(E, rows, K, dtype=dtype, device=dev)
-            B.moe_mx_dequantize(at + c, stride, at + s, B.MX_ROWS, stride, B.MX_FP4, E, rows, K, o,
-                                dt, K, rows * K, stream)
-            outs.append(o)
+    at, stride = w.blobs.data_ptr(), w.blobs.stride(0)
+    outs = []
+    for c, s, rows, K in _blob_planes(w.hidden, w.inter):
+        o = torch.empty(E, rows, K, dtype=dtype, device=dev)
+        _call("moe_mx_dequantize", dev, stream, at + c, stride, at + s, B.MX_ROWS, stride,
+              B.MX_FP4, E, rows, K, o.data_ptr(), dt, K, rows * K)
+        outs.append(o)
     return tuple(outs)
