@@ -154,9 +154,11 @@ STRATA_DEVFN uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(saddr), "r"(rank));
   return ra;
 }
+// Arrive on another CTA's barrier.  For hand-overs that order tensor memory
+// (by its own fences), not ordinary memory: a release at cluster scope would
+// wait a thousand cycles and more for the thread's global writes.
 STRATA_DEVFN void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 STRATA_DEVFN void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
