@@ -339,7 +339,9 @@ cudaError_t launch_linear(const MxLinearArgs& a, cudaStream_t st) {
       splits = s;
     }
   }
-  const int S = (long long)tn * tt * splits <= a.num_sms ? C::S1 : C::S2;
+  // Clusters of 4 and 8 do not fill every SM of a GPC: at one CTA an SM some
+  // would wait for a second turn (N = 1024, K = 4096, T = 256: 14 us for 9).
+  const int S = splits <= 2 && tn * tt * splits <= a.num_sms ? C::S1 : C::S2;
   auto kern = mx_linear_kernel<XF, WF, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(S));
   if (e != cudaSuccess) return e;
@@ -363,11 +365,15 @@ cudaError_t launch_linear(const MxLinearArgs& a, cudaStream_t st) {
 template <int XF, int WF>
 cudaError_t launch_linear_t(const MxLinearArgs& a, cudaStream_t st) {
   // Token tiles of a call start at multiples of 128 (a scale tile's rows) or
-  // there is one: the smallest that holds T.
+  // there is one: the smallest that holds T.  Past 128 tokens these tiles are
+  // taken while every SM gets at most one; beyond that the pairs' 256 x 256
+  // tiles, with half of the copies, win.  K = 4096, 8x4 bits, N = 4096: 12.0 us
+  // here against 13.9 at T = 256; N = 16384: 21.4 against 16.5.
   if (a.T <= 16) return launch_linear<XF, WF, 16>(a, st);
   if (a.T <= 32) return launch_linear<XF, WF, 32>(a, st);
   if (a.T <= 64) return launch_linear<XF, WF, 64>(a, st);
-  if (a.T <= 128) return launch_linear<XF, WF, 128>(a, st);
+  if (a.T <= 128 || mx_ceil(a.T, 128) * mx_ceil(a.N, kLM) <= a.num_sms)
+    return launch_linear<XF, WF, 128>(a, st);
   return launch_mx_gemm(a, st);
 }
 
