@@ -6,7 +6,10 @@
 // One CTA a row, the row in registers between the sum of squares and the
 // output, so every input is read once and every output written once: bound by
 // HBM for many rows, by the launch and one load-reduce-store chain for few.
-// Sums are fp32 in a fixed order (per thread, warp butterfly, warp partials).
+// A thread's up to 32 squares are summed in fp32, the threads' sums in fp64
+// (fixed order: warp butterfly, warp partials), which leaves the mean to one
+// rounding: a code next to a border between two then goes the way of the
+// exact norm as often as 32 bits allow.
 #include "mx.cuh"
 #include "tc05.cuh"
 
@@ -55,7 +58,7 @@ STRATA_DEVFN void store8_as(void* p, int dt, int64_t i, const float (&v)[8]) {
 // VPT groups of 8 elements a thread: group threadIdx.x + blockDim.x * j.
 template <int VPT>
 __global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a) {
-  __shared__ float red[kNMaxThreads / 32];
+  __shared__ double red[kNMaxThreads / 32];
   const int tid = threadIdx.x, nth = blockDim.x;
   const int G = a.H / 8;
   const int kt = (a.H + 127) / 128;
@@ -81,12 +84,14 @@ load_groups_as<VPT>(a.x, a.x_dtype, base, G, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(r[j][i], r[j][i], ss);
     }
-    ss = warp_sum(ss);
-    if ((tid & 31) == 0) red[tid >> 5] = ss;
+    double sum = ss;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((tid & 31) == 0) red[tid >> 5] = sum;
     __syncthreads();
-    ss = 0.f;
-    for (int w = 0; w < nth / 32; ++w) ss += red[w];
-    const float inv = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+    sum = 0.;
+    for (int w = 0; w < nth / 32; ++w) sum += red[w];
+    const float inv = rsqrtf((float)sum * (1.0f / (float)a.H) + a.eps);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int g = tid + nth * j;

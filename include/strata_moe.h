@@ -446,7 +446,7 @@ STRATA_API int32_t moe_mx_tile_scales(const void* scales, int32_t rows, int32_t 
  *   written.  Where codes are written, scales [T, H/32] go in scale_layout.
  * Limits: T >= 0 (0: no-op), H in 32..16384, a multiple of 8, of 32 where
  * codes are written.  All pointers 16-byte aligned (scales by rows: any).
- * The sum of squares is fp32 in a fixed order: the same bits on every run. */
+ * The sum of squares is taken in a fixed order: the same bits on every run. */
 STRATA_API int32_t moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* delta,
                         int32_t delta_dtype, const float* gain, int32_t T, int32_t H, float eps,
                         void* residual_out, void* out, int32_t out_dtype, int32_t mx_fmt,
