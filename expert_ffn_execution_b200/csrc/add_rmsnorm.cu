@@ -5,7 +5,11 @@
 //
 // One CTA a row, the row in registers between the sum of squares and the
 // output, so every input is read once and every output written once: bound by
-// HBM for many rows, by the launch and one load-reduce-store chain for few.
+// HBM for many rows (T = 8192, H = 4096, fp32 + bf16 to bf16 and FP8: 66.9 us,
+// 6.5 TB/s), by the launch and one load-reduce-store chain for few.  CTAs that
+// take rows in turn, with the next rows copied ahead, are slower (98 us): a
+// row's two reductions are the wait, and many CTAs hide it better than a few.
+//
 // A thread's up to 32 squares are summed in fp32, the threads' sums in fp64
 // (fixed order: warp butterfly, warp partials), which leaves the mean to one
 // rounding: a code next to a border between two then goes the way of the
@@ -19,8 +23,7 @@ namespace {
 
 constexpr int kNMaxThreads = 512;
 
-// The row's groups of this thread, loaded before the first is used (the type
-// is looked at outside the loop, which leaves the loads free to overlap).
+// The row's groups of this thread, loaded before the first is used.
 template <int DT, int VPT>
 STRATA_DEVFN void load_groups(const void* p, int64_t base, int G, float (&v)[VPT][8]) {
   constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
@@ -37,15 +40,6 @@ STRATA_DEVFN void load_groups(const void* p, int64_t base, int G, float (&v)[VPT
 #pragma unroll
   for (int j = 0; j < VPT; ++j) raw[j].values(v[j]);
 }
-template <int VPT>
-STRATA_DEVFN void load_groups_as(const void* p, int dt, int64_t base, int G, float (&v)[VPT][8]) {
-  if (dt == STRATA_DTYPE_F32)
-    load_groups<STRATA_DTYPE_F32>(p, base, G, v);
-  else if (dt == STRATA_DTYPE_F16)
-    load_groups<STRATA_DTYPE_F16>(p, base, G, v);
-  else
-    load_groups<STRATA_DTYPE_BF16>(p, base, G, v);
-}
 STRATA_DEVFN void store8_as(void* p, int dt, int64_t i, const float (&v)[8]) {
   if (dt == STRATA_DTYPE_F32)
     store8<STRATA_DTYPE_F32>(reinterpret_cast<float*>(p) + i, v);
@@ -55,8 +49,9 @@ STRATA_DEVFN void store8_as(void* p, int dt, int64_t i, const float (&v)[8]) {
     store8<STRATA_DTYPE_BF16>(reinterpret_cast<uint16_t*>(p) + i, v);
 }
 
-// VPT groups of 8 elements a thread: group threadIdx.x + blockDim.x * j.
-template <int VPT>
+// VPT groups of 8 elements a thread: group threadIdx.x + blockDim.x * j.  XT,
+// DT: dtypes of x and delta (DT < 0: no delta).
+template <int XT, int DT, int VPT>
 __global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a) {
   __shared__ double red[kNMaxThreads / 32];
   const int tid = threadIdx.x, nth = blockDim.x;
@@ -68,10 +63,10 @@ __global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a
     const int64_t base = (int64_t)row * a.H;
     float r[VPT][8];
     float ss = 0.f;
-load_groups_as<VPT>(a.x, a.x_dtype, base, G, r);
-    if (a.delta) {
+    load_groups<XT>(a.x, base, G, r);
+    if constexpr (DT >= 0) {
       float d[VPT][8];
-      load_groups_as<VPT>(a.delta, a.delta_dtype, base, G, d);
+      load_groups<DT>(a.delta, base, G, d);
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
 #pragma unroll
@@ -80,7 +75,10 @@ load_groups_as<VPT>(a.x, a.x_dtype, base, G, r);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int g = tid + nth * j;
-      if (a.residual_out && g < G) store8_as(a.residual_out, a.x_dtype, base + 8 * g, r[j]);
+      if (a.residual_out && g < G)
+        store8<XT>(reinterpret_cast<uint8_t*>(a.residual_out) +
+                       (base + 8 * g) * (XT == STRATA_DTYPE_F32 ? 4 : 2),
+                   r[j]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(r[j][i], r[j][i], ss);
     }
@@ -89,8 +87,10 @@ load_groups_as<VPT>(a.x, a.x_dtype, base, G, r);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if ((tid & 31) == 0) red[tid >> 5] = sum;
     __syncthreads();
-    sum = 0.;
-    for (int w = 0; w < nth / 32; ++w) sum += red[w];
+    sum = (tid & 31) < nth / 32 ? red[tid & 31] : 0.;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum = __shfl_sync(0xffffffffu, sum, 0);
     const float inv = rsqrtf((float)sum * (1.0f / (float)a.H) + a.eps);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -142,7 +142,7 @@ load_groups_as<VPT>(a.x, a.x_dtype, base, G, r);
   }
 }
 
-template <int VPT>
+template <int XT, int DT, int VPT>
 cudaError_t launch_norm(const AddNormArgs& a, int rows, int threads, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -153,7 +153,25 @@ cudaError_t launch_norm(const AddNormArgs& a, int rows, int threads, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, add_rmsnorm_kernel<VPT>, a);
+  return cudaLaunchKernelEx(&cfg, add_rmsnorm_kernel<XT, DT, VPT>, a);
+}
+
+template <int XT, int VPT>
+cudaError_t launch_norm_d(const AddNormArgs& a, int rows, int threads, cudaStream_t st) {
+  if (!a.delta) return launch_norm<XT, -1, VPT>(a, rows, threads, st);
+  if (a.delta_dtype == STRATA_DTYPE_F32)
+    return launch_norm<XT, STRATA_DTYPE_F32, VPT>(a, rows, threads, st);
+  if (a.delta_dtype == STRATA_DTYPE_F16)
+    return launch_norm<XT, STRATA_DTYPE_F16, VPT>(a, rows, threads, st);
+  return launch_norm<XT, STRATA_DTYPE_BF16, VPT>(a, rows, threads, st);
+}
+template <int VPT>
+cudaError_t launch_norm_x(const AddNormArgs& a, int rows, int threads, cudaStream_t st) {
+  if (a.x_dtype == STRATA_DTYPE_F32)
+    return launch_norm_d<STRATA_DTYPE_F32, VPT>(a, rows, threads, st);
+  if (a.x_dtype == STRATA_DTYPE_F16)
+    return launch_norm_d<STRATA_DTYPE_F16, VPT>(a, rows, threads, st);
+  return launch_norm_d<STRATA_DTYPE_BF16, VPT>(a, rows, threads, st);
 }
 
 }  // namespace
@@ -162,12 +180,16 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t st) {
   const int rows = a.fmt && a.layout == STRATA_MX_TILES
                        ? (int)(mx_ceil(a.T, kMxTileRows) * kMxTileRows)
                        : a.T;
+  // One group a thread, or two (32 bytes of a 16-bit x) where there are rows
+  // enough to fill the SMs: T = 4096, H = 4096, bf16 to FP4 24.4 us with one,
+  // 21.5 with two; T = 16: 2.5 and 2.8; fp32 rows 66.9 and 67.8 (T = 8192).
   const int G = a.H / 8;
-  const int vpt = G <= kNMaxThreads ? 1 : G <= 2 * kNMaxThreads ? 2 : 4;
+  int vpt = a.x_dtype != STRATA_DTYPE_F32 && a.T > 148 ? 2 : 1;
+  while (G > vpt * kNMaxThreads) vpt *= 2;
   const int threads = (((G + vpt - 1) / vpt) + 31) & ~31;
-  if (vpt == 1) return launch_norm<1>(a, rows, threads, st);
-  if (vpt == 2) return launch_norm<2>(a, rows, threads, st);
-  return launch_norm<4>(a, rows, threads, st);
+  if (vpt == 1) return launch_norm_x<1>(a, rows, threads, st);
+  if (vpt == 2) return launch_norm_x<2>(a, rows, threads, st);
+  return launch_norm_x<4>(a, rows, threads, st);
 }
 
 }  // namespace strata
