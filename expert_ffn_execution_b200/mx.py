@@ -40,18 +40,22 @@ def _device(first, *others):
     return dev
 
 
-def _call(name, dev, stream, *args):
-    """The library's `name` on `dev`, on `stream` (None: its current stream)."""
+def _enter(dev, stream):
+    """(library, stream handle) for a call on `dev`, which must be current:
+    `stream` as a handle, or the device's current stream."""
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev.index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    fn = getattr(B._lib or B.load(), name)
-    if dev.index == torch._C._cuda_getDevice():
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, stream)
+    return B._lib or B.load(), stream
+
+
+def _elsewhere(dev) -> bool:
+    """Whether `dev` is not the current device."""
+    return dev.index != torch._C._cuda_getDevice()
+
+
+def _check(name, rc):
     if rc:
         raise B.StrataError(name, rc)
 
@@ -130,9 +134,14 @@ class MXTensor:
     def dequantize(self, dtype=torch.float32, stream=None) -> torch.Tensor:
         """The matrix's values: [rows, K] of `dtype`."""
         dt, dev = _dtype(dtype), _device(self)
+        if _elsewhere(dev):
+            with torch.cuda.device(dev):
+                return self.dequantize(dtype, stream)
+        lib, stream = _enter(dev, stream)
         out = torch.empty(self.rows, self.K, dtype=dtype, device=dev)
-        _call("moe_mx_dequantize", dev, stream, self.codes_ptr, 0, self.scales_ptr, self.layout, 0,
-              self.fmt, 1, self.rows, self.K, out.data_ptr(), dt, self.K, 0)
+        rc = lib.moe_mx_dequantize(self.codes_ptr, 0, self.scales_ptr, self.layout, 0, self.fmt, 1,
+                                   self.rows, self.K, out.data_ptr(), dt, self.K, 0, stream)
+        _check("moe_mx_dequantize", rc)
         return out
 
 
@@ -149,9 +158,14 @@ def mx_quantize(x: torch.Tensor, fmt: int, layout: int = B.MX_TILES, stream=None
     if K < 32 or K % 32:
         raise ValueError(f"K = {K}: a positive multiple of 32 is wanted")
     dev = _device(x)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return mx_quantize(x, fmt, layout, stream)
+    lib, stream = _enter(dev, stream)
     q = MXTensor._empty(fmt, rows, K, layout, dev)
-    _call("moe_mx_quantize", dev, stream, ptr, dt, 1, rows, K, stride, 0, fmt, q.codes_ptr, 0,
-          q.scales_ptr, layout, 0)
+    rc = lib.moe_mx_quantize(ptr, dt, 1, rows, K, stride, 0, fmt, q.codes_ptr, 0, q.scales_ptr,
+                             layout, 0, stream)
+    _check("moe_mx_quantize", rc)
     return q
 
 
@@ -160,8 +174,13 @@ def mx_tile_scales(q: MXTensor, stream=None) -> MXTensor:
     if q.layout == B.MX_TILES:
         return q
     dev = _device(q)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return mx_tile_scales(q, stream)
+    lib, stream = _enter(dev, stream)
     tiles = torch.empty(_scale_bytes(q.rows, q.K, B.MX_TILES), dtype=torch.uint8, device=dev)
-    _call("moe_mx_tile_scales", dev, stream, q.scales_ptr, q.rows, q.K, tiles.data_ptr())
+    rc = lib.moe_mx_tile_scales(q.scales_ptr, q.rows, q.K, tiles.data_ptr(), stream)
+    _check("moe_mx_tile_scales", rc)
     return MXTensor(q.codes, tiles, q.fmt, q.rows, q.K, B.MX_TILES)
 
 
@@ -196,14 +215,19 @@ def add_rmsnorm(x: torch.Tensor, delta: torch.Tensor | None = None,
     xd, dd = _dtype(x.dtype), 0 if delta is None else _dtype(delta.dtype)
     od = 0 if out_dtype is None else _dtype(out_dtype)
     dev = _device(x, delta, gain, residual_out)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return add_rmsnorm(x, delta, gain, eps, out_dtype, fmt, layout, residual_out, stream)
+    lib, stream = _enter(dev, stream)
     res = residual_out
     if res is None and delta is not None:
         res = torch.empty_like(x)
     out = None if out_dtype is None else torch.empty(T, H, dtype=out_dtype, device=dev)
     q = MXTensor._empty(fmt, T, H, layout, dev) if fmt else None
-    _call("moe_add_rmsnorm", dev, stream, x.data_ptr(), xd, _ptr(delta), dd, _ptr(gain), T, H, eps,
-          _ptr(res), _ptr(out), od, fmt, q.codes_ptr if fmt else None,
-          q.scales_ptr if fmt else None, layout)
+    rc = lib.moe_add_rmsnorm(x.data_ptr(), xd, _ptr(delta), dd, _ptr(gain), T, H, eps, _ptr(res),
+                             _ptr(out), od, fmt, q.codes_ptr if fmt else None,
+                             q.scales_ptr if fmt else None, layout, stream)
+    _check("moe_add_rmsnorm", rc)
     return AddNorm(x if res is None else res, out, q)
 
 
@@ -232,10 +256,15 @@ def mx_linear(x: MXTensor, w: MXTensor, bias: torch.Tensor | None = None,
             ldy = out.stride(0)
     dt = _dtype(out_dtype)
     dev = _device(x, w, bias, out, dev_status)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return mx_linear(x, w, bias, out_dtype, out, dev_status, stream)
+    lib, stream = _enter(dev, stream)
     if out is None:
         out = torch.empty(T, N, dtype=out_dtype, device=dev)
-    _call("moe_mx_linear", dev, stream, x.codes_ptr, x.fmt, x.scales_ptr, T, w.codes_ptr, w.fmt,
-          w.scales_ptr, N, K, _ptr(bias), out.data_ptr(), dt, ldy, _ptr(dev_status))
+    rc = lib.moe_mx_linear(x.codes_ptr, x.fmt, x.scales_ptr, T, w.codes_ptr, w.fmt, w.scales_ptr,
+                           N, K, _ptr(bias), out.data_ptr(), dt, ldy, _ptr(dev_status), stream)
+    _check("moe_mx_linear", rc)
     return out
 
 
@@ -266,12 +295,17 @@ def pack_experts(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
                 w.data_ptr() % 16:
             raise ValueError("weights must have contiguous rows that start on 16-byte boundaries")
     dts, dev = [_dtype(w.dtype) for w in ws], _device(*ws)
-    stride = B.strata_expert_bytes(B.FMT_MXFP4_32, H, I)
-    blobs = torch.empty(E, stride, dtype=torch.uint8, device=dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return pack_experts(gate, up, down, stream)
+    lib, stream = _enter(dev, stream)
+    size = B.strata_expert_bytes(B.FMT_MXFP4_32, H, I)
+    blobs = torch.empty(E, size, dtype=torch.uint8, device=dev)
     at = blobs.data_ptr()
     for w, dt, (c, s, rows, K) in zip(ws, dts, _blob_planes(H, I)):
-        _call("moe_mx_quantize", dev, stream, w.data_ptr(), dt, E, rows, K, w.stride(1),
-              w.stride(0), B.MX_FP4, at + c, stride, at + s, B.MX_ROWS, stride)
+        rc = lib.moe_mx_quantize(w.data_ptr(), dt, E, rows, K, w.stride(1), w.stride(0), B.MX_FP4,
+                                 at + c, size, at + s, B.MX_ROWS, size, stream)
+        _check("moe_mx_quantize", rc)
     return ExpertWeights(blobs, B.FMT_MXFP4_32, H, I)
 
 
@@ -280,11 +314,16 @@ def unpack_experts(w: ExpertWeights, dtype=torch.float32, stream=None):
     if w.fmt != B.FMT_MXFP4_32:
         raise ValueError("only MXFP4 blobs are read back")
     dt, dev, E = _dtype(dtype), _device(w.blobs), w.num_experts
-    at, stride = w.blobs.data_ptr(), w.blobs.stride(0)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return unpack_experts(w, dtype, stream)
+    lib, stream = _enter(dev, stream)
+    at, size = w.blobs.data_ptr(), w.blobs.stride(0)
     outs = []
     for c, s, rows, K in _blob_planes(w.hidden, w.inter):
         o = torch.empty(E, rows, K, dtype=dtype, device=dev)
-        _call("moe_mx_dequantize", dev, stream, at + c, stride, at + s, B.MX_ROWS, stride,
-              B.MX_FP4, E, rows, K, o.data_ptr(), dt, K, rows * K)
+        rc = lib.moe_mx_dequantize(at + c, size, at + s, B.MX_ROWS, size, B.MX_FP4, E, rows, K,
+                                   o.data_ptr(), dt, K, rows * K, stream)
+        _check("moe_mx_dequantize", rc)
         outs.append(o)
     return tuple(outs)
