@@ -11,10 +11,14 @@
 // The 128-row operand is the weights and the columns are the tokens, so a few
 // tokens cost a few columns: with T tokens the call has to stream N*K codes,
 // which bounds it by HBM up to a few hundred tokens.  A CTA owns 128 features
-// x NT tokens; where there are fewer tiles than SMs the K axis is split over
-// a cluster of up to 8 CTAs, whose partial sums are joined through
-// distributed shared memory in rank order.
+// x NT tokens; where there are fewer tiles than SMs the K axis is split over a
+// cluster of up to 8 CTAs, and every CTA joins the sums of some of the tokens
+// in rank order.  Joining is a matter of round trips: T = 4, N = 2560, K =
+// 2560, 8x4 bits takes 5.2 us when the sums are fetched, 16 bytes at a time,
+// behind a barrier that orders memory, and 4.5 us now that each CTA sends a
+// rank its tokens by one bulk copy that counts on the receiver's barrier.
 #include <algorithm>
+#include <cmath>
 
 #include "deal.h"
 #include "mx_mma.cuh"
@@ -26,7 +30,6 @@ namespace {
 
 constexpr int kLThreads = 192;  // warps 0-3 epilogue, 4 copies, 5 MMA
 constexpr int kLM = 128;        // features a tile
-constexpr int kLBatch = 2;      // joined pieces in flight a thread
 constexpr long long kLDrainCycles = 40000000LL;
 
 template <int XF, int WF, int NT>
@@ -44,17 +47,24 @@ struct LinCfg {
   static constexpr int sfcols = 8 * ST;  // tensor-memory columns of a stage's scales
   static constexpr int dcols = NT < 32 ? 32 : NT;
   static constexpr int head = 1024;      // barriers, and the alignment of what follows
-  // Stages of a CTA that has its SM to itself, and of one that shares it with
-  // another (shared memory, and with it tensor memory, split in two).
-  static constexpr int S1 = (227 * 1024 - head - 1024) / stride;
-  static constexpr int S2 = (113 * 1024 - head - 1024) / stride;
-  static constexpr int smem(int S) { return S * stride + head + 1024; }
+  static constexpr int token = kLM * 4;  // bytes of a token's sums
+  // Stages of a CTA with `room` bytes; a split K also takes the sums that are
+  // sent to it.
+  static constexpr int stages(int room, bool split) {
+    return (room - head - 1024 - (split ? NT * token : 0)) / stride;
+  }
+  static constexpr int kAlone = 227 * 1024, kShared = 113 * 1024;  // one CTA an SM, two
+  static constexpr int smem(int S, bool split) {
+    return S * stride + head + 1024 + (split ? NT * token : 0);
+  }
   static constexpr int cols(int S) {
     return dcols + S * sfcols <= 64 ? 64 : dcols + S * sfcols <= 128 ? 128 : 256;
   }
-  static_assert(dcols + S1 * sfcols <= 256, "at most half of the tensor memory");
-  static_assert(S2 >= 2 && S2 * stride >= NT * kLM * 4, "the partial sums fit");
-  static_assert((2 * S1 + 1) * 8 + 16 <= head, "the barriers fit");
+  static_assert(dcols + stages(kAlone, false) * sfcols <= 256, "at most half of the tensor memory");
+  static_assert(stages(kShared, false) * stride >= NT * token, "the sums fit over the stages");
+  static_assert(NT == 128 || (stages(kShared, true) * stride >= NT * token &&
+                              stages(kShared, true) >= 3), "and with a split K");
+  static_assert((2 * stages(kAlone, false) + 2) * 8 + 16 <= head, "the barriers fit");
 };
 
 // Four consecutive values of a row of y; `vec`: the row's pieces of four are
@@ -83,15 +93,13 @@ STRATA_DEVFN void store4(void* y, int64_t i, const float (&v)[4], int n, bool ve
   }
 }
 
-// The ranks' sums -> y.  Rank r joins tokens r, r + splits, ...: a thread four
-// features of one, kLBatch of them at a time with all ranks' loads in flight.
-template <int DT, int NT>
-STRATA_DEVFN void write_y(const MxLinearArgs& a, const uint8_t* smem, int n0, int t0, int rank,
-                          int splits) {
+// Sums [rank][token][feature], ranks `per` tokens apart, of `count` tokens from
+// t0 on -> y: a thread four features of one, rank by rank.
+template <int DT>
+STRATA_DEVFN void write_y(const MxLinearArgs& a, const uint8_t* sums, int n0, int t0, int count,
+                          int per, int splits) {
   constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
-  const int nt = min(NT, a.T - t0);
-  const int items = nt > rank ? ((nt - rank - 1) / splits + 1) * (kLM / 4) : 0;
-  const uint32_t base = smem_addr(smem);
+  const int items = count * (kLM / 4), rank_bytes = per * kLM * 4;
   const bool vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * kEl) == 0;
   // a thread's feature is the same in all of its items
   static_assert(kLThreads % 32 == 0, "items of a thread are whole tokens apart");
@@ -102,45 +110,19 @@ STRATA_DEVFN void write_y(const MxLinearArgs& a, const uint8_t* smem, int n0, in
     for (int k = 0; k < 4; ++k)
       if (k < left) bias[k] = a.bias[n + k];
   }
-  void* const y = a.y;
-  if (splits == 1) {
 #pragma unroll 1
-    for (int i = threadIdx.x; i < items; i += kLThreads) {
-      const float4 v = *reinterpret_cast<const float4*>(smem + 4u * (uint32_t)((i / 32) * kLM + f));
-      const float s[4] = {v.x + bias[0], v.y + bias[1], v.z + bias[2], v.w + bias[3]};
-      store4<DT>(y, (int64_t)(t0 + i / 32) * a.ldy + n, s, left, vec);
+  for (int i = threadIdx.x; i < items; i += kLThreads) {
+    const uint8_t* at = sums + 4 * ((i / 32) * kLM + f);
+    float4 v = *reinterpret_cast<const float4*>(at);
+    for (int q = 1; q < splits; ++q) {
+      const float4 u = *reinterpret_cast<const float4*>(at + q * rank_bytes);
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
     }
-    return;
-  }
-#pragma unroll 1
-  for (int i0 = threadIdx.x; i0 < items; i0 += kLThreads * kLBatch) {
-    float4 v[kLBatch][8];
-#pragma unroll
-    for (int b = 0; b < kLBatch; ++b) {
-      const int i = i0 + b * kLThreads;
-      const uint32_t at = base + 4u * (uint32_t)((rank + (i / 32) * splits) * kLM + f);
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < splits && i < items) v[b][q] = ld_cluster_f32x4(cluster_addr(at, q));
-    }
-#pragma unroll
-    for (int b = 0; b < kLBatch; ++b) {
-      const int i = i0 + b * kLThreads;
-      if (i >= items) break;
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (q < splits) {
-          s[0] += v[b][q].x;
-          s[1] += v[b][q].y;
-          s[2] += v[b][q].z;
-          s[3] += v[b][q].w;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[k] += bias[k];
-      store4<DT>(y, (int64_t)(t0 + rank + (i / 32) * splits) * a.ldy + n, s, left, vec);
-    }
+    const float s[4] = {v.x + bias[0], v.y + bias[1], v.z + bias[2], v.w + bias[3]};
+    store4<DT>(a.y, (int64_t)(t0 + i / 32) * a.ldy + n, s, left, vec);
   }
 }
 
@@ -156,7 +138,8 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
   uint64_t* full = reinterpret_cast<uint64_t*>(smem0);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+  uint64_t* joined = tfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* issued = reinterpret_cast<int*>(tmem_slot + 2);
 
@@ -168,15 +151,16 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
   const int c0 = (int)((long long)chunks * rank / splits);
   const int nch = (int)((long long)chunks * (rank + 1) / splits) - c0;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    mbar_init(tfull, 1);
+  // the tile's tokens, and those that this rank joins: [rank per, rank per + mine)
+  const int nt = min(NT, a.T - t0), per = (nt + splits - 1) / splits;
+  const int first = (int)rank * per, mine = max(0, min(per, nt - first));
+  if ((int)threadIdx.x < 2 * S + 2) {  // one barrier a thread: in turn they took 0.4 us
+    mbar_init(&full[threadIdx.x], 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == kLThreads - 1) {
     *abort_flag = 0;
     *issued = 0;
-    fence_barrier_init();
   }
   if (warp == 4 && lane == 0) {
     prefetch_tensormap(&wmap);
@@ -190,6 +174,12 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  if (splits > 1) {
+    if (threadIdx.x == 0)  // every rank sends this one its sums of `mine` tokens
+      mbar_arrive_expect_tx(joined, (uint32_t)(mine * splits * C::token));
+    __syncwarp();
+    cluster_arrive_relaxed();  // waited for before the first copy to another rank
+  }
   pdl_wait_prior();
 
   if (warp == 4) {
@@ -231,7 +221,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
         tc_fence_after();
         const int left = a.K - (c0 + i) * C::KS;  // a multiple of 128
         const uint32_t st = stages + (uint32_t)(s * C::stride);
+        // a tile that starts 64 tokens into its scale tile reads two columns on
         const uint32_t sfw = tbase + C::dcols + s * C::sfcols, sfx = sfw + 4 * C::ST;
+        const uint32_t sfx_at = sfx + (NT == 64 ? (t0 % 128) / 32 : 0);
 #pragma unroll
         for (int b = 0; b < C::ST; ++b) {
           if (b * 128 < left) {
@@ -248,7 +240,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
             const int b = C::F4 ? j / 2 : 0;
             const uint32_t sf = C::F4 ? 2u * (j & 1) : (uint32_t)j;
             mma_mx<C::F4>(tbase, wlo + 2 * j, xlo + 2 * j, hi, idesc_mx(wf, xf, kLM, NT, sf),
-                          sfw + 4 * b, sfx + 4 * b, (uint32_t)(i + j > 0));
+                          sfw + 4 * b, sfx_at + 4 * b, (uint32_t)(i + j > 0));
           }
         }
         mma_commit(&empty[s]);
@@ -274,6 +266,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
         for (int i = 0; i < 16; ++i) red[(c + i) * kLM + f] = __uint_as_float(r[i]);
       }
     }
+    if (splits > 1) fence_proxy_async_smem();  // read by the bulk copies
     tc_fence_before();
   }
   __syncthreads();
@@ -286,15 +279,34 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     mbar_wait_bounded(tfull, 0, a.status, kLDrainCycles);
   }
   __syncwarp();
-  if (splits > 1) cluster_sync_all();  // every rank's sums are written
-  if (a.y_dtype == STRATA_DTYPE_F32)
-    write_y<STRATA_DTYPE_F32, NT>(a, smem, n0, t0, rank, splits);
-  else if (a.y_dtype == STRATA_DTYPE_F16)
-    write_y<STRATA_DTYPE_F16, NT>(a, smem, n0, t0, rank, splits);
-  else
-    write_y<STRATA_DTYPE_BF16, NT>(a, smem, n0, t0, rank, splits);
+  const uint8_t* sums = smem;
+  bool ok = true;
+  if (splits > 1) {
+    cluster_wait();
+    sums = smem + S * C::stride;
+    if ((int)threadIdx.x < splits) {
+      const int to = threadIdx.x, count = min(per, nt - to * per);
+      if (count > 0)
+        bulk_s2cluster(cluster_addr(smem_addr(sums) + (int)rank * per * C::token, to),
+                       smem_addr(smem) + to * per * C::token, (uint32_t)(count * C::token),
+                       cluster_addr(smem_addr(joined), to));
+    }
+    __syncwarp();
+    // not guarded by the abort flag: every rank sends, and what is on its way
+    // here has to land before this CTA goes
+    ok = mbar_wait_bounded(joined, 0, a.status);
+    __syncwarp();
+  }
+  if (ok) {
+    if (a.y_dtype == STRATA_DTYPE_F32)
+      write_y<STRATA_DTYPE_F32>(a, sums, n0, t0 + first, mine, per, splits);
+    else if (a.y_dtype == STRATA_DTYPE_F16)
+      write_y<STRATA_DTYPE_F16>(a, sums, n0, t0 + first, mine, per, splits);
+    else
+      write_y<STRATA_DTYPE_BF16>(a, sums, n0, t0 + first, mine, per, splits);
+  }
   __syncwarp();
-  if (splits > 1) cluster_sync_relaxed();  // nobody leaves while its sums are read
+  if (splits > 1) cluster_sync_relaxed();  // nobody leaves while its sums are being sent
   if (warp == 5) {
     tc_fence_after();
     tmem_dealloc(tbase, C::cols(S));
@@ -313,43 +325,26 @@ bool make_mx_map(CUtensorMap* map, const uint8_t* codes, int fmt, bool spread, i
 }
 
 template <int XF, int WF, int NT>
-cudaError_t launch_linear(const MxLinearArgs& a, cudaStream_t st) {
+cudaError_t launch_linear(const MxLinearArgs& a, int splits, cudaStream_t st) {
   using C = LinCfg<XF, WF, NT>;
   CUtensorMap wmap, xmap;
   if (!make_mx_map(&wmap, a.w_codes, WF, C::kSpread, a.N, a.K, kLM) ||
       !make_mx_map(&xmap, a.x_codes, XF, false, a.T, a.K, NT))
     return cudaErrorInvalidValue;
   const int tn = (a.N + kLM - 1) / kLM, tt = (a.T + NT - 1) / NT;
-  const int chunks = (a.K + C::KS - 1) / C::KS;
-  // Split K where that ends sooner.  A stage costs its SM its 128-byte rows
-  // (about 0.2 us at 16 tokens: 2.5 cycles a row), whichever CTA it belongs
-  // to; joining costs about 9 such stages and one more for 8 tokens.  N =
-  // 2560, K = 8192, T = 4, 8x4 bits: 16.0, 11.0, 8.0 and 7.1 us with 1, 2, 4
-  // and 8 ranks; N = 8192, K = 2048: 6.2, 6.4, 6.7 and 11.7.
-  const double stage_cost = (kLM + NT) / 144.0 * (C::F4 ? 1.25 : 1.0);
-  int splits = 1;
-  double best = 0;
-  for (int s = 1; s <= 8; s *= 2) {
-    const double ctas = (double)tn * tt * s;
-    if (s > 1 && (ctas > 2.0 * a.num_sms || chunks < 2 * s)) break;
-    const double cost = (chunks + s - 1) / s * stage_cost * std::max(1.0, ctas / a.num_sms) +
-                        (s > 1 ? 8 + NT / 8 + (s == 8 ? 2 : 0) : 0);
-    if (s == 1 || cost < best) {
-      best = cost;
-      splits = s;
-    }
-  }
+  const bool split = splits > 1;
   // Clusters of 4 and 8 do not fill every SM of a GPC: at one CTA an SM some
   // would wait for a second turn (N = 1024, K = 4096, T = 256: 14 us for 9).
-  const int S = splits <= 2 && tn * tt * splits <= a.num_sms ? C::S1 : C::S2;
+  const bool alone = splits <= 2 && (int64_t)tn * tt * splits <= a.num_sms;
+  const int S = C::stages(alone ? C::kAlone : C::kShared, split);
   auto kern = mx_linear_kernel<XF, WF, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(S));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(S, split));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(tn * splits, tt);
   cfg.blockDim = dim3(kLThreads);
-  cfg.dynamicSmemBytes = C::smem(S);
+  cfg.dynamicSmemBytes = C::smem(S, split);
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -362,19 +357,54 @@ cudaError_t launch_linear(const MxLinearArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, wmap, xmap, a, splits, S);
 }
 
+// Tokens a tile and ranks a tile, by what they cost in units of the 0.2 us
+// that a stage of 128 weight rows and 16 token rows takes its SM (2.5 cycles a
+// 128-byte row, whichever CTA it belongs to).  Measured, T = 4, 8x4 bits, with
+// 1, 2, 4 and 8 ranks: N = 2560, K = 8192 15.4, 9.8, 6.6 and 6.2 us; N = 1024,
+// K = 2560 6.7, 5.4, 4.5 and 4.2; N = 8192, K = 2048 6.0, 5.3 and 5.6.
+struct LinPlan {
+  int nt, splits;
+};
+LinPlan plan_linear(int T, int N, int K, bool f4, int num_sms) {
+  // Tiles of 16 and 32 tokens are for calls with one: a tile starts at a
+  // multiple of 64 (its scales at a tensor-memory column of their own).
+  const int lo = T <= 16 ? 16 : T <= 32 ? 32 : 64, hi = T <= 64 ? lo : 128;
+  const int chunks = (int)mx_ceil(K, f4 ? 256 : 128);
+  LinPlan best = {lo, 1};
+  double least = 0;
+  for (int nt = lo; nt <= hi; nt *= 2) {
+    const int64_t tiles = mx_ceil(N, kLM) * mx_ceil(T, nt);
+    for (int s = 1; s <= 8; s *= 2) {
+      const int64_t ctas = tiles * s;
+      // (the sums of 128 tokens twice over leave no room for a second CTA)
+      if (s > 1 && (nt == 128 || ctas > 2 * num_sms || chunks < 2 * s)) break;
+      const double full = (double)ctas / num_sms;
+      const double busy = full <= 1 ? 1 : (full + std::ceil(full)) / 2;
+      const double stage = (kLM + nt) / 144.0 * (f4 ? 1.25 : 1.0);
+      const double join = s == 1 ? 0 : (1.5 + 0.11 * nt) * (s == 2 ? 1 : s == 4 ? 1.25 : 1.4) +
+                                           (s == 8 && full > 1 ? 4 : 0);
+      const double cost = mx_ceil(chunks, s) * stage * busy + join + nt / 16.0;
+      if ((nt == lo && s == 1) || cost < least) {
+        least = cost;
+        best = {nt, s};
+      }
+    }
+  }
+  return best;
+}
+
 template <int XF, int WF>
 cudaError_t launch_linear_t(const MxLinearArgs& a, cudaStream_t st) {
-  // Token tiles of a call start at multiples of 128 (a scale tile's rows) or
-  // there is one: the smallest that holds T.  Past 128 tokens these tiles are
-  // taken while every SM gets at most one; beyond that the pairs' 256 x 256
-  // tiles, with half of the copies, win.  K = 4096, 8x4 bits, N = 4096: 12.0 us
-  // here against 13.9 at T = 256; N = 16384: 21.4 against 16.5.
-  if (a.T <= 16) return launch_linear<XF, WF, 16>(a, st);
-  if (a.T <= 32) return launch_linear<XF, WF, 32>(a, st);
-  if (a.T <= 64) return launch_linear<XF, WF, 64>(a, st);
-  if (a.T <= 128 || mx_ceil(a.T, 128) * mx_ceil(a.N, kLM) <= a.num_sms)
-    return launch_linear<XF, WF, 128>(a, st);
-  return launch_mx_gemm(a, st);
+  // Past 128 tokens these tiles are taken while every SM gets at most one of
+  // 128 x 128; beyond that the pairs' 256 x 256 tiles, with half of the
+  // copies, win.  K = 4096, 8x4 bits, N = 4096: 12.0 us here against 13.9 at
+  // T = 256; N = 16384: 21.4 against 16.5.
+  if (a.T > 128 && mx_ceil(a.T, 128) * mx_ceil(a.N, kLM) > a.num_sms) return launch_mx_gemm(a, st);
+  const LinPlan p = plan_linear(a.T, a.N, a.K, XF == STRATA_MX_FP4 && WF == STRATA_MX_FP4, a.num_sms);
+  if (p.nt == 16) return launch_linear<XF, WF, 16>(a, p.splits, st);
+  if (p.nt == 32) return launch_linear<XF, WF, 32>(a, p.splits, st);
+  if (p.nt == 64) return launch_linear<XF, WF, 64>(a, p.splits, st);
+  return launch_linear<XF, WF, 128>(a, p.splits, st);
 }
 
 }  // namespace

@@ -160,28 +160,32 @@ STRATA_DEVFN uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
 STRATA_DEVFN void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-STRATA_DEVFN void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+// The cluster's barrier, in two steps, without ordering memory: for mbarriers
+// made visible by their own fence, and for shared memory that only has to stay allocated.
+// (A release waits for the CTA's outstanding global writes: 0.5 us and more.)
+STRATA_DEVFN void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+STRATA_DEVFN void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same without ordering memory: for barriers made visible by their own
-// fence, and for shared memory that only has to stay allocated.  (The release
-// above waits for the CTA's outstanding global writes: 0.5 us and more.)
 STRATA_DEVFN void cluster_sync_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive_relaxed();
+  cluster_wait();
 }
 STRATA_DEVFN uint32_t cluster_ctarank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-STRATA_DEVFN float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
+// Bulk copy of this CTA's shared memory into another's (`dst`, `bar`: their
+// shared::cluster addresses), counted in bytes on that CTA's barrier.
+STRATA_DEVFN void bulk_s2cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+      "[%3];" ::"r"(dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 }  // namespace strata
