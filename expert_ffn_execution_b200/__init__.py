@@ -11,8 +11,9 @@ from ._binding import (DECODE_MAX_T, DEV_BOUNDS, DEV_TIMEOUT, DTYPE_BF16, DTYPE_
                        moe_add_rmsnorm, moe_bucket, moe_bucket_workspace_size, moe_combine,
                        moe_experts, moe_experts_static_scratch, moe_gather_rows,
                        moe_experts_workspace_size, moe_layer_forward, moe_layer_workspace_size,
-                       moe_mx_dequantize, moe_mx_linear, moe_mx_quantize, moe_mx_scale_bytes,
-                       moe_mx_tile_scales, moe_rmsnorm, moe_route, moe_route_workspace_size, moe_router_topk,
+                       moe_mx_dequantize, moe_mx_linear, moe_mx_pack_experts, moe_mx_quantize,
+                       moe_mx_scale_bytes, moe_mx_tile_scales, moe_mx_unpack_experts,
+                       moe_rmsnorm, moe_route, moe_route_workspace_size, moe_router_topk,
                        moe_router_topk_workspace_size,
                        moe_shared_expert, moe_shared_expert_workspace_size, qweights,
                        status_string, strata_expert_bytes, strata_read_status,

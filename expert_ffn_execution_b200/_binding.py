@@ -74,6 +74,8 @@ _SIGS = {
     "moe_mx_scale_bytes": (_U64, [_I, _I, _I]),
     "moe_mx_quantize": (_I, [_P, _I, _I, _I, _I, _I64, _I64, _I, _P, _U64, _P, _I, _U64, _P]),
     "moe_mx_dequantize": (_I, [_P, _U64, _P, _I, _U64, _I, _I, _I, _I, _P, _I, _I64, _I64, _P]),
+    "moe_mx_pack_experts": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _U64, _P]),
+    "moe_mx_unpack_experts": (_I, [_P, _U64, _I, _I, _I, _P, _P, _P, _I, _P]),
     "moe_mx_tile_scales": (_I, [_P, _I, _I, _P, _P]),
     "moe_add_rmsnorm": (_I, [_P, _I, _P, _I, _P, _I, _I, _F, _P, _P, _I, _I, _P, _P, _I, _P]),
     "moe_mx_linear": (_I, [_P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _I, _I64, _P, _P]),
@@ -279,6 +281,25 @@ def moe_mx_dequantize(codes, codes_batch_stride, scales, scale_layout, scales_ba
                                   scales_batch_stride, fmt, batch, rows, K, _ptr(dst), dst_dtype,
                                   dst_row_stride, dst_batch_stride, _stream(stream))
     return _check("moe_mx_dequantize", rc) if check else rc
+
+
+def _i64x3(v):
+    return None if v is None else (_I64 * 3)(*v)
+
+
+def moe_mx_pack_experts(gate, up, down, dtype, row_strides, expert_strides, E, H, I, blobs,
+                        blob_stride, stream=None, check=True):
+    rc = load().moe_mx_pack_experts(_ptr(gate), _ptr(up), _ptr(down), dtype, _i64x3(row_strides),
+                                    _i64x3(expert_strides), E, H, I, _ptr(blobs), blob_stride,
+                                    _stream(stream))
+    return _check("moe_mx_pack_experts", rc) if check else rc
+
+
+def moe_mx_unpack_experts(blobs, blob_stride, E, H, I, gate, up, down, dtype, stream=None,
+                          check=True):
+    rc = load().moe_mx_unpack_experts(_ptr(blobs), blob_stride, E, H, I, _ptr(gate), _ptr(up),
+                                      _ptr(down), dtype, _stream(stream))
+    return _check("moe_mx_unpack_experts", rc) if check else rc
 
 
 def moe_mx_tile_scales(scales, rows, K, tiles, stream=None, check=True):

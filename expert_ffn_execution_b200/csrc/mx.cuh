@@ -194,7 +194,8 @@ struct MxQuantArgs {
   int layout;
   uint64_t scales_stride;  // bytes between matrices
 };
-cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t st);
+// n <= 3 batches of one dtype and format in one launch.
+cudaError_t launch_mx_quantize(const MxQuantArgs* a, int n, cudaStream_t st);
 
 struct MxDequantArgs {
   const uint8_t* codes;
@@ -208,7 +209,7 @@ struct MxDequantArgs {
   int dst_dtype;
   int64_t row_stride, batch_stride;  // elements
 };
-cudaError_t launch_mx_dequantize(const MxDequantArgs& a, cudaStream_t st);
+cudaError_t launch_mx_dequantize(const MxDequantArgs* a, int n, cudaStream_t st);
 cudaError_t launch_mx_tile_scales(const uint8_t* src, int64_t rows, int64_t K, uint8_t* dst,
                                   cudaStream_t st);
 

@@ -2,6 +2,7 @@
 // checks and launches.  See include/strata_moe.h.
 #include "abi_util.h"
 #include "mx.cuh"
+#include "qformat.cuh"
 
 using namespace strata;
 
@@ -37,6 +38,16 @@ int32_t check_batch(const void* data, int32_t dtype, int64_t row_stride, int64_t
   return STRATA_OK;
 }
 
+// The blobs of E MXFP4 experts.
+int32_t check_experts(int32_t E, int32_t H, int32_t I, const void* blobs, uint64_t stride) {
+  if (E < 0 || H < 128 || I < 128 || H % 128 || I % 128) return STRATA_EINVAL;
+  uint64_t total = 0;
+  plane_offsets(STRATA_FMT_MXFP4_32, H, I, &total);
+  if (stride % 256 || stride < total) return STRATA_EINVAL;
+  if (E > 0 && (!blobs || !aligned(blobs, 256))) return STRATA_EINVAL;
+  return STRATA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -68,7 +79,7 @@ int32_t moe_mx_quantize(const void* src, int32_t src_dtype, int32_t batch, int32
   a.scales = reinterpret_cast<uint8_t*>(scales);
   a.layout = scale_layout;
   a.scales_stride = scales_batch_stride;
-  return from_cuda(launch_mx_quantize(a, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_mx_quantize(&a, 1, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int32_t moe_mx_dequantize(const void* codes, uint64_t codes_batch_stride, const void* scales,
@@ -98,7 +109,71 @@ int32_t moe_mx_dequantize(const void* codes, uint64_t codes_batch_stride, const 
   a.dst_dtype = dst_dtype;
   a.row_stride = dst_row_stride;
   a.batch_stride = dst_batch_stride;
-  return from_cuda(launch_mx_dequantize(a, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_mx_dequantize(&a, 1, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int32_t moe_mx_pack_experts(const void* gate, const void* up, const void* down, int32_t dtype,
+                            const int64_t* row_strides, const int64_t* expert_strides, int32_t E,
+                            int32_t H, int32_t I, void* blobs, uint64_t blob_stride,
+                            void* stream) {
+  const int32_t r = check_experts(E, H, I, blobs, blob_stride);
+  if (r != STRATA_OK) return r;
+  if (E == 0) return STRATA_OK;
+  if (!row_strides || !expert_strides) return STRATA_EINVAL;
+  const Planes pl = plane_offsets(STRATA_FMT_MXFP4_32, H, I);
+  const void* src[3] = {gate, up, down};
+  MxQuantArgs a[3] = {};
+  for (int i = 0; i < 3; ++i) {
+    a[i].src = src[i];
+    a[i].src_dtype = dtype;
+    a[i].batch = E;
+    a[i].rows = i < 2 ? I : H;
+    a[i].K = i < 2 ? H : I;
+    a[i].row_stride = row_strides[i];
+    a[i].batch_stride = expert_strides[i];
+    a[i].fmt = STRATA_MX_FP4;
+    a[i].codes = reinterpret_cast<uint8_t*>(blobs) + pl.codes[i];
+    a[i].codes_stride = blob_stride;
+    a[i].scales = reinterpret_cast<uint8_t*>(blobs) + pl.scales[i];
+    a[i].layout = STRATA_MX_ROWS;
+    a[i].scales_stride = blob_stride;
+    const int32_t c = check_batch(src[i], dtype, a[i].row_stride, a[i].batch_stride, E,
+                                  (int32_t)a[i].rows, (int32_t)a[i].K, a[i].fmt, a[i].codes,
+                                  blob_stride, a[i].scales, a[i].layout, blob_stride);
+    if (c != STRATA_OK) return c;
+  }
+  return from_cuda(launch_mx_quantize(a, 3, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int32_t moe_mx_unpack_experts(const void* blobs, uint64_t blob_stride, int32_t E, int32_t H,
+                              int32_t I, void* gate, void* up, void* down, int32_t dtype,
+                              void* stream) {
+  const int32_t r = check_experts(E, H, I, blobs, blob_stride);
+  if (r != STRATA_OK) return r;
+  if (E == 0) return STRATA_OK;
+  const Planes pl = plane_offsets(STRATA_FMT_MXFP4_32, H, I);
+  void* dst[3] = {gate, up, down};
+  MxDequantArgs a[3] = {};
+  for (int i = 0; i < 3; ++i) {
+    a[i].codes = reinterpret_cast<const uint8_t*>(blobs) + pl.codes[i];
+    a[i].codes_stride = blob_stride;
+    a[i].scales = reinterpret_cast<const uint8_t*>(blobs) + pl.scales[i];
+    a[i].layout = STRATA_MX_ROWS;
+    a[i].scales_stride = blob_stride;
+    a[i].fmt = STRATA_MX_FP4;
+    a[i].batch = E;
+    a[i].rows = i < 2 ? I : H;
+    a[i].K = i < 2 ? H : I;
+    a[i].dst = dst[i];
+    a[i].dst_dtype = dtype;
+    a[i].row_stride = a[i].K;
+    a[i].batch_stride = (int64_t)H * I;
+    const int32_t c = check_batch(dst[i], dtype, a[i].row_stride, a[i].batch_stride, E,
+                                  (int32_t)a[i].rows, (int32_t)a[i].K, a[i].fmt, a[i].codes,
+                                  blob_stride, a[i].scales, a[i].layout, blob_stride);
+    if (c != STRATA_OK) return c;
+  }
+  return from_cuda(launch_mx_dequantize(a, 3, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int32_t moe_mx_tile_scales(const void* scales, int32_t rows, int32_t K, void* tiles, void* stream) {

@@ -27,9 +27,11 @@ namespace {
 constexpr int kGEpi = 8;                       // warps that read the sums
 constexpr int kGThreads = (kGEpi + 2) * 32;
 constexpr int kGM = 256, kGN = 256;            // a pair's tile
+constexpr int kGPitch = 69;                    // words between rows in store_shifted
 constexpr long long kGDrainCycles = 40000000LL;
 
-template <int XF, int WF>
+// ANY: rows of y need not start on 16-byte boundaries.
+template <int XF, int WF, bool ANY>
 struct GemmCfg {
   static constexpr bool F4 = XF == STRATA_MX_FP4 && WF == STRATA_MX_FP4;
   static constexpr bool kSpread = WF == STRATA_MX_FP4 && !F4;
@@ -40,19 +42,104 @@ struct GemmCfg {
   static constexpr int SA = ST * kMxTileBytes, SBb = 2 * SA;     // scales of 128 and 256 rows
   static constexpr int stage = AB + BB + SA + SBb;
   static constexpr int stride = (stage + 1023) / 1024 * 1024;
-  static constexpr int epi = kGEpi * 32 * 64;
+  static constexpr int epi = kGEpi * 32 * (ANY ? 4 * kGPitch : 64);
   static constexpr int S = (227 * 1024 - 2048 - epi) / stride;
   static constexpr int smem = S * stride + epi + 2048;
   static constexpr int sfcols = 12 * ST;
   static_assert(kGN + S * sfcols <= 512, "sums and scales fit the tensor memory");
 };
 
-template <int XF, int WF, int DT>
+// A pass's 64 bytes of `rows` rows, a word a lane, side by side, where rows end
+// inside (`left` bytes of them are y's).
+template <int EL>
+STRATA_DEVFN void store_rows(const uint8_t* buf, uint8_t* y, int64_t pitch, int rows, int left,
+                             int lane) {
+  const int at = lane % 16 * 4;
+  if (at >= left) return;
+#pragma unroll 4
+  for (int g = 0; g < 16; ++g) {
+    const int row = g * 2 + lane / 16;
+    const uint8_t* src = buf + row * 64 + (((at / 16) ^ (row / 2)) & 3) * 16 + at % 16;
+    uint8_t* dst = y + row * pitch + at;
+    if (row < rows) {
+      if (EL == 4 || at + 4 <= left)
+        *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+      else  // the first of the last pair
+        *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+    }
+  }
+}
+
+// Up to 256 bytes of 32 rows, a row a lane in w, to rows `pitch` apart that
+// start at y on any boundary of EL bytes: each row is shifted in shared memory
+// to how it lies in 16-byte pieces of memory, whole pieces are stored as such
+// and the (up to two) others element by element.  `left` bytes of a row are
+// y's.  Element by element throughout, the stores took longer than the MMAs:
+// T = 1452, N = 25295, K = 640, 4x4 bits 49 us, now 32 us, and 24 us with N =
+// 25296, whose rows are on 16-byte boundaries.
+template <int EL>
+STRATA_DEVFN void store_shifted(uint32_t* buf, const uint32_t* w, uint8_t* y, int64_t pitch,
+                                int rows, int left, int lane) {
+  left = min(left, 256);
+  if (left <= 0 || rows <= 0) return;
+  auto low = [&](int row) {  // where in a piece a row starts
+    return (int)((reinterpret_cast<uintptr_t>(y) + (uintptr_t)(row * pitch)) & 15);
+  };
+  {
+    const int s = low(lane);
+    // an odd number of 2-byte elements: words of the high half of one and the
+    // low half of the next
+    const bool half = EL == 2 && (s & 2);
+    const uint32_t sel = half ? 0x5432u : 0x7654u;
+    uint32_t* to = buf + lane * kGPitch + s / 4;
+    __syncwarp();
+    to[0] = __byte_perm(0u, w[0], sel);
+#pragma unroll
+    for (int i = 1; i < 64; ++i) to[i] = __byte_perm(w[i - 1], w[i], sel);
+    if (half) to[64] = w[63] >> 16;
+    __syncwarp();
+  }
+  // Whole pieces: 16 lanes a row (the 17th piece of a row is never whole).
+  {
+    const int pc = lane % 16;
+    uint8_t* at = y + (lane / 16) * pitch + pc * 16;
+    const uint32_t* v = buf + (lane / 16) * kGPitch + pc * 4;
+#pragma unroll 4
+    for (int row = lane / 16; row < 32; row += 2, at += 2 * pitch, v += 2 * kGPitch) {
+      const int s = low(row);
+      if (row < rows && pc * 16 >= s && pc * 16 + 16 <= s + left)
+        *reinterpret_cast<uint4*>(at - s) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  // The others: a lane an element of a row's first or last piece, rows side by
+  // side (a row a lane cost the store unit 32 lines an instruction).
+  {
+    constexpr int kPiece = 16 / EL, kRows = 32 / (2 * kPiece);
+    const int end = lane % (2 * kPiece) / kPiece, e = lane % kPiece * EL;
+    uint8_t* to = y + lane / (2 * kPiece) * pitch;
+#pragma unroll 4
+    for (int row = lane / (2 * kPiece); row < 32; row += kRows, to += kRows * pitch) {
+      const int s = low(row), last = s + left;
+      const int at = (end ? last / 16 * 16 : 0) + e;  // from the row's first piece
+      // none: a whole first piece; a first piece that is the last; a whole last one
+      const bool some = end ? last % 16 != 0 : s != 0 && last >= 16;
+      if (row < rows && some && at >= s && at + EL <= last) {
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(buf + row * kGPitch) + at;
+        if constexpr (EL == 4)
+          *reinterpret_cast<uint32_t*>(to + (at - s)) = *reinterpret_cast<const uint32_t*>(src);
+        else
+          *reinterpret_cast<uint16_t*>(to + (at - s)) = *reinterpret_cast<const uint16_t*>(src);
+      }
+    }
+  }
+}
+
+template <int XF, int WF, int DT, bool ANY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                const __grid_constant__ CUtensorMap xsmap, const __grid_constant__ CUtensorMap wsmap,
-               MxLinearArgs a, int mt, int tiles, int vec) {
-  using C = GemmCfg<XF, WF>;
+               MxLinearArgs a, int mt, int tiles) {
+  using C = GemmCfg<XF, WF, ANY>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -171,10 +258,10 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   } else {
     // ------------------------------------------------ sums -> y
     const int q = warp % 4, half = warp / 4;
-    uint8_t* buf = epi + warp * (32 * 64);
+    uint8_t* buf = epi + warp * (C::epi / kGEpi);
     const uint32_t lead = cluster_addr(smem_addr(tempty), 0);
     constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
-    constexpr int kPer = 64 / kEl;   // features a pass
+    constexpr int kPer = 64 / kEl;   // features a pass of aligned rows
     int it = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++it) {
       const int t0 = (tile % mt) * kGM + 128 * (int)rank + 32 * q;
@@ -200,12 +287,19 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         for (int i = 0; i < 64; ++i)
           r[i] = pack2<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
       }
+      const int rows = min(32, a.T - t0);
+      uint8_t* const yb = reinterpret_cast<uint8_t*>(a.y) + ((int64_t)t0 * a.ldy + n0) * kEl;
+      if constexpr (ANY) {
+#pragma unroll
+        for (int p = 0; p < kEl / 2; ++p)
+          store_shifted<kEl>(reinterpret_cast<uint32_t*>(buf), r + 64 * p, yb + 256 * p,
+                             a.ldy * kEl, rows, (a.N - n0) * kEl - 256 * p, lane);
+        continue;
+      }
       // 64 bytes of each of the 32 rows at a time through shared memory, the
       // 16-byte pieces of row r at places piece ^ (r/2 % 4): both the writes
       // (a row a lane) and the reads (four lanes a row) touch every bank once
-      const int rows = min(32, a.T - t0);
-      uint8_t* const yb = reinterpret_cast<uint8_t*>(a.y) + ((int64_t)t0 * a.ldy + n0) * kEl;
-      const bool whole = vec && n0 + 128 <= a.N && rows > 0;
+      const bool whole = n0 + 128 <= a.N;
       const int row = lane / 4, pc = lane % 4;
 #pragma unroll
       for (int p = 0; p < 128 / kPer; ++p) {
@@ -225,19 +319,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                   *reinterpret_cast<const uint4*>(buf + (g * 8 + row) * 64 +
                                                   ((pc ^ (row / 2)) & 3) * 16);
         } else {
-          // rows without 16-byte boundaries, or the last features: a lane a feature
-          const int left = min(kPer, a.N - n0 - p * kPer);
-#pragma unroll 1
-          for (int w = 0; w < rows; ++w) {
-            if (lane >= left) continue;
-            const int at = lane * kEl;
-            const uint8_t* src = buf + w * 64 + (((at / 16) ^ (w / 2)) & 3) * 16 + at % 16;
-            uint8_t* dst = yb + (int64_t)w * a.ldy * kEl + p * 64 + at;
-            if constexpr (kEl == 4)
-              *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
-            else
-              *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
-          }
+          store_rows<kEl>(buf, yb + p * 64, a.ldy * kEl, rows, (a.N - n0 - p * kPer) * kEl, lane);
         }
       }
     }
@@ -282,9 +364,9 @@ bool make_scale_map(CUtensorMap* map, const uint8_t* scales, int rows, int K, in
                    CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <int XF, int WF, int DT>
+template <int XF, int WF, int DT, bool ANY>
 cudaError_t launch_gemm(const MxLinearArgs& a, cudaStream_t st) {
-  using C = GemmCfg<XF, WF>;
+  using C = GemmCfg<XF, WF, ANY>;
   CUtensorMap xmap, wmap, xsmap, wsmap;
   if (!make_code_map(&xmap, a.x_codes, XF, false, a.T, a.K) ||
       !make_code_map(&wmap, a.w_codes, WF, C::kSpread, a.N, a.K) ||
@@ -293,9 +375,7 @@ cudaError_t launch_gemm(const MxLinearArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int mt = (a.T + kGM - 1) / kGM, nt = (a.N + kGN - 1) / kGN;
   const int tiles = mt * nt;
-  constexpr int el = DT == STRATA_DTYPE_F32 ? 4 : 2;
-  const int vec = (reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy * el % 16 == 0) ? 1 : 0;
-  auto kern = mx_gemm_kernel<XF, WF, DT>;
+  auto kern = mx_gemm_kernel<XF, WF, DT, ANY>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -308,14 +388,21 @@ cudaError_t launch_gemm(const MxLinearArgs& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, xmap, wmap, xsmap, wsmap, a, mt, tiles, vec);
+  return cudaLaunchKernelEx(&cfg, kern, xmap, wmap, xsmap, wsmap, a, mt, tiles);
+}
+
+template <int XF, int WF, int DT>
+cudaError_t launch_gemm_rows(const MxLinearArgs& a, cudaStream_t st) {
+  constexpr int el = DT == STRATA_DTYPE_F32 ? 4 : 2;
+  const bool aligned = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy * el % 16 == 0;
+  return aligned ? launch_gemm<XF, WF, DT, false>(a, st) : launch_gemm<XF, WF, DT, true>(a, st);
 }
 
 template <int XF, int WF>
 cudaError_t launch_gemm_y(const MxLinearArgs& a, cudaStream_t st) {
-  if (a.y_dtype == STRATA_DTYPE_F32) return launch_gemm<XF, WF, STRATA_DTYPE_F32>(a, st);
-  if (a.y_dtype == STRATA_DTYPE_F16) return launch_gemm<XF, WF, STRATA_DTYPE_F16>(a, st);
-  return launch_gemm<XF, WF, STRATA_DTYPE_BF16>(a, st);
+  if (a.y_dtype == STRATA_DTYPE_F32) return launch_gemm_rows<XF, WF, STRATA_DTYPE_F32>(a, st);
+  if (a.y_dtype == STRATA_DTYPE_F16) return launch_gemm_rows<XF, WF, STRATA_DTYPE_F16>(a, st);
+  return launch_gemm_rows<XF, WF, STRATA_DTYPE_BF16>(a, st);
 }
 
 }  // namespace

@@ -67,62 +67,67 @@ struct LinCfg {
   static_assert((2 * stages(kAlone, false) + 2) * 8 + 16 <= head, "the barriers fit");
 };
 
-// Four consecutive values of a row of y; `vec`: the row's pieces of four are
-// aligned for one store.
 template <int DT>
-STRATA_DEVFN void store4(void* y, int64_t i, const float (&v)[4], int n, bool vec) {
-  if constexpr (DT == STRATA_DTYPE_F32) {
-    float* p = reinterpret_cast<float*>(y) + i;
-    if (vec && n == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < n) p[k] = v[k];
-    }
-  } else {
-    uint16_t* p = reinterpret_cast<uint16_t*>(y) + i;
-    const uint32_t lo = pack2<DT>(v[0], v[1]), hi = pack2<DT>(v[2], v[3]);
-    if (vec && n == 4) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < n) p[k] = (uint16_t)((k < 2 ? lo : hi) >> (16 * (k & 1)));
-    }
-  }
+STRATA_DEVFN void store1(void* y, int64_t i, float v) {
+  if constexpr (DT == STRATA_DTYPE_F32)
+    reinterpret_cast<float*>(y)[i] = v;
+  else
+    reinterpret_cast<uint16_t*>(y)[i] = (uint16_t)pack2<DT>(v, v);
+}
+template <int DT>
+STRATA_DEVFN void store4(void* y, int64_t i, const float (&v)[4]) {
+  if constexpr (DT == STRATA_DTYPE_F32)
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(y) + i) =
+        make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(y) + i) =
+        make_uint2(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]));
 }
 
 // Sums [rank][token][feature], ranks `per` tokens apart, of `count` tokens from
-// t0 on -> y: a thread four features of one, rank by rank.
+// t0 on -> y, rank by rank.  A lane has four features of a token: adjacent
+// ones, stored together, where all rows of the tile are aligned for that and
+// inside y, else ones 32 apart, so that the lanes' stores are side by side.
 template <int DT>
 STRATA_DEVFN void write_y(const MxLinearArgs& a, const uint8_t* sums, int n0, int t0, int count,
                           int per, int splits) {
   constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
-  const int items = count * (kLM / 4), rank_bytes = per * kLM * 4;
-  const bool vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * kEl) == 0;
-  // a thread's feature is the same in all of its items
-  static_assert(kLThreads % 32 == 0, "items of a thread are whole tokens apart");
-  const int f = threadIdx.x % 32 * 4, n = n0 + f, left = min(4, a.N - n);
+  const int rank_floats = per * kLM, left = a.N - n0;
+  const bool vec = left >= kLM && a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * kEl) == 0;
+  const int lane = threadIdx.x % 32, f0 = vec ? 4 * lane : lane, df = vec ? 1 : 32;
   float bias[4] = {0.f, 0.f, 0.f, 0.f};
   if (a.bias) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (k < left) bias[k] = a.bias[n + k];
+      if (f0 + k * df < left) bias[k] = a.bias[n0 + f0 + k * df];
   }
-#pragma unroll 1
-  for (int i = threadIdx.x; i < items; i += kLThreads) {
-    const uint8_t* at = sums + 4 * ((i / 32) * kLM + f);
-    float4 v = *reinterpret_cast<const float4*>(at);
-    for (int q = 1; q < splits; ++q) {
-      const float4 u = *reinterpret_cast<const float4*>(at + q * rank_bytes);
-      v.x += u.x;
-      v.y += u.y;
-      v.z += u.z;
-      v.w += u.w;
+#pragma unroll 2
+  for (int t = threadIdx.x / 32; t < count; t += kLThreads / 32) {
+    const float* at = reinterpret_cast<const float*>(sums) + t * kLM + f0;
+    const int64_t o = (int64_t)(t0 + t) * a.ldy + n0 + f0;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+      for (int q = 0; q < splits; ++q) {
+        const float4 u = *reinterpret_cast<const float4*>(at + q * rank_floats);
+        v[0] += u.x;
+        v[1] += u.y;
+        v[2] += u.z;
+        v[3] += u.w;
+      }
+    } else {
+      for (int q = 0; q < splits; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] += at[q * rank_floats + 32 * k];
     }
-    const float s[4] = {v.x + bias[0], v.y + bias[1], v.z + bias[2], v.w + bias[3]};
-    store4<DT>(a.y, (int64_t)(t0 + i / 32) * a.ldy + n, s, left, vec);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += bias[k];
+    if (vec) {
+      store4<DT>(a.y, o, v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (f0 + 32 * k < left) store1<DT>(a.y, o + 32 * k, v[k]);
+    }
   }
 }
 

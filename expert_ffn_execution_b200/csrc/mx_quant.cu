@@ -100,16 +100,39 @@ STRATA_DEVFN int64_t scale_at(const Place& p, int layout, uint64_t batch_stride,
          (layout == STRATA_MX_TILES ? mx_tile_byte((int)p.row, blk, kt) : p.row * blocks + blk);
 }
 
+// Up to three batches a launch (the planes of expert blobs), one after the
+// other over the grid: batch i has blocks first[i] .. first[i + 1] - 1.
+template <typename Args>
+struct Jobs {
+  Args a[3];
+  Walk w[3];
+  Stride src[3], dst[3];
+  uint32_t first[4];
+};
+template <typename Args>
+STRATA_DEVFN int job_of(const Jobs<Args>& j) {
+  return (blockIdx.x >= j.first[1]) + (blockIdx.x >= j.first[2]);
+}
+// The places of this thread's pieces.
+template <typename Args>
+STRATA_DEVFN void places_of(const Jobs<Args>& jobs, int j, Place (&p)[kQUnroll]) {
+  const Walk& w = jobs.w[j];
+  const uint64_t block = blockIdx.x - jobs.first[j];
+  p[0] = first_place(w, jobs.src[j], jobs.dst[j], block * (kQThreads * kQUnroll) + threadIdx.x);
+#pragma unroll
+  for (int u = 1; u < kQUnroll; ++u) p[u] = next_place(w, jobs.src[j], jobs.dst[j], p[u - 1]);
+}
+
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(MxQuantArgs a, Walk w, Stride ss,
-                                                                Stride sd) {
+__global__ void __launch_bounds__(kQThreads)
+mx_quantize_kernel(const __grid_constant__ Jobs<MxQuantArgs> jobs) {
+  const int j = job_of(jobs);
+  const MxQuantArgs& a = jobs.a[j];
   const uint32_t pieces = (uint32_t)(a.K / kQEl);
   const int kt = (int)mx_ceil(a.K, kMxTileBlocks * kMxBlock);
   const uint8_t* src = reinterpret_cast<const uint8_t*>(a.src);
   Place p[kQUnroll];
-  p[0] = first_place(w, ss, sd, (uint64_t)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x);
-#pragma unroll
-  for (int u = 1; u < kQUnroll; ++u) p[u] = next_place(w, ss, sd, p[u - 1]);
+  places_of(jobs, j, p);
   pdl_wait_prior();
   Raw8<DT> raw[kQUnroll][2];
 #pragma unroll
@@ -144,15 +167,15 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(MxQuantArgs a, W
 }
 
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(MxDequantArgs a, Walk w,
-                                                                  Stride ss, Stride sd) {
+__global__ void __launch_bounds__(kQThreads)
+mx_dequantize_kernel(const __grid_constant__ Jobs<MxDequantArgs> jobs) {
   constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
+  const int j = job_of(jobs);
+  const MxDequantArgs& a = jobs.a[j];
   const int kt = (int)mx_ceil(a.K, kMxTileBlocks * kMxBlock);
   uint8_t* dst = reinterpret_cast<uint8_t*>(a.dst);
   Place p[kQUnroll];
-  p[0] = first_place(w, ss, sd, (uint64_t)blockIdx.x * (kQThreads * kQUnroll) + threadIdx.x);
-#pragma unroll
-  for (int u = 1; u < kQUnroll; ++u) p[u] = next_place(w, ss, sd, p[u - 1]);
+  places_of(jobs, j, p);
   pdl_wait_prior();
   uint2 c0[kQUnroll], c1[kQUnroll];
   uint32_t e[kQUnroll];
@@ -170,7 +193,7 @@ __global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(MxDequantArgs 
       c0[u] = make_uint2(c.x, c.y);
       c1[u] = make_uint2(c.z, c.w);
     }
-    e[u] = a.scales[scale_at(p[u], a.layout, a.scales_stride, w.per / 2, kt)];
+    e[u] = a.scales[scale_at(p[u], a.layout, a.scales_stride, jobs.w[j].per / 2, kt)];
   }
   // The two lanes of a block trade halves of their codes, so that both write
   // the first lane's 16 elements side by side, then the second's: with 16
@@ -214,11 +237,10 @@ __global__ void __launch_bounds__(kQThreads) mx_tile_scales_kernel(const uint8_t
 }
 
 template <typename Kern, typename... A>
-cudaError_t launch_groups(Kern kern, uint64_t total, uint64_t per_cta, cudaStream_t st,
-                          A... args) {
+cudaError_t launch_blocks(Kern kern, uint64_t blocks, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)((total + per_cta - 1) / per_cta));
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kQThreads);
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -228,21 +250,37 @@ cudaError_t launch_groups(Kern kern, uint64_t total, uint64_t per_cta, cudaStrea
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Fills in where each job's blocks are; false where the grid would be too large.
+template <typename Args>
+bool deal_blocks(Jobs<Args>& j, int n) {
+  uint64_t at = 0;
+  for (int i = 0; i < 4; ++i) {
+    j.first[i] = (uint32_t)at;
+    if (i < n) at += (uint64_t)mx_ceil((int64_t)j.w[i].total, kQThreads * kQUnroll);
+    if (at >= (uint64_t)1 << 31) return false;
+  }
+  return true;
+}
+
 }  // namespace
 
-cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t st) {
-  // with tiles, the padding rows and blocks of the scale tiles are visited too
-  const bool tiles = a.layout == STRATA_MX_TILES;
-  const Walk w = make_walk(a.batch, tiles ? mx_ceil(a.rows, kMxTileRows) * kMxTileRows : a.rows,
-                           tiles ? mx_ceil(a.K, 128) * (128 / kQEl) : a.K / kQEl);
-  const int64_t el = a.src_dtype == STRATA_DTYPE_F32 ? 4 : 2;
-  const Stride ss = make_stride(w, a.batch_stride * el, a.row_stride * el, kQEl * el);
-  const Stride sd = make_stride(w, (int64_t)a.codes_stride, mx_row_bytes(a.fmt, a.K),
-                                mx_row_bytes(a.fmt, kQEl));
-  constexpr uint64_t cta = kQThreads * kQUnroll;
-#define STRATA_Q(DT, FMT)                 \
-  if (a.src_dtype == DT && a.fmt == FMT)  \
-    return launch_groups(mx_quantize_kernel<DT, FMT>, w.total, cta, st, a, w, ss, sd);
+cudaError_t launch_mx_quantize(const MxQuantArgs* a, int n, cudaStream_t st) {
+  Jobs<MxQuantArgs> j = {};
+  for (int i = 0; i < n; ++i) {
+    // with tiles, the padding rows and blocks of the scale tiles are visited too
+    const bool tiles = a[i].layout == STRATA_MX_TILES;
+    const int64_t el = a[i].src_dtype == STRATA_DTYPE_F32 ? 4 : 2;
+    j.a[i] = a[i];
+    j.w[i] = make_walk(a[i].batch, tiles ? mx_ceil(a[i].rows, kMxTileRows) * kMxTileRows : a[i].rows,
+                       tiles ? mx_ceil(a[i].K, 128) * (128 / kQEl) : a[i].K / kQEl);
+    j.src[i] = make_stride(j.w[i], a[i].batch_stride * el, a[i].row_stride * el, kQEl * el);
+    j.dst[i] = make_stride(j.w[i], (int64_t)a[i].codes_stride, mx_row_bytes(a[i].fmt, a[i].K),
+                           mx_row_bytes(a[i].fmt, kQEl));
+  }
+  if (!deal_blocks(j, n)) return cudaErrorInvalidValue;
+#define STRATA_Q(DT, FMT)                     \
+  if (a->src_dtype == DT && a->fmt == FMT)    \
+    return launch_blocks(mx_quantize_kernel<DT, FMT>, j.first[3], st, j);
   STRATA_Q(STRATA_DTYPE_F32, STRATA_MX_FP4)
   STRATA_Q(STRATA_DTYPE_F16, STRATA_MX_FP4)
   STRATA_Q(STRATA_DTYPE_BF16, STRATA_MX_FP4)
@@ -253,16 +291,20 @@ cudaError_t launch_mx_quantize(const MxQuantArgs& a, cudaStream_t st) {
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_mx_dequantize(const MxDequantArgs& a, cudaStream_t st) {
-  const Walk w = make_walk(a.batch, a.rows, a.K / kQEl);
-  const int64_t el = a.dst_dtype == STRATA_DTYPE_F32 ? 4 : 2;
-  const Stride ss = make_stride(w, (int64_t)a.codes_stride, mx_row_bytes(a.fmt, a.K),
-                                mx_row_bytes(a.fmt, kQEl));
-  const Stride sd = make_stride(w, a.batch_stride * el, a.row_stride * el, kQEl * el);
-  constexpr uint64_t cta = kQThreads * kQUnroll;
-#define STRATA_D(DT, FMT)                 \
-  if (a.dst_dtype == DT && a.fmt == FMT)  \
-    return launch_groups(mx_dequantize_kernel<DT, FMT>, w.total, cta, st, a, w, ss, sd);
+cudaError_t launch_mx_dequantize(const MxDequantArgs* a, int n, cudaStream_t st) {
+  Jobs<MxDequantArgs> j = {};
+  for (int i = 0; i < n; ++i) {
+    const int64_t el = a[i].dst_dtype == STRATA_DTYPE_F32 ? 4 : 2;
+    j.a[i] = a[i];
+    j.w[i] = make_walk(a[i].batch, a[i].rows, a[i].K / kQEl);
+    j.src[i] = make_stride(j.w[i], (int64_t)a[i].codes_stride, mx_row_bytes(a[i].fmt, a[i].K),
+                           mx_row_bytes(a[i].fmt, kQEl));
+    j.dst[i] = make_stride(j.w[i], a[i].batch_stride * el, a[i].row_stride * el, kQEl * el);
+  }
+  if (!deal_blocks(j, n)) return cudaErrorInvalidValue;
+#define STRATA_D(DT, FMT)                     \
+  if (a->dst_dtype == DT && a->fmt == FMT)    \
+    return launch_blocks(mx_dequantize_kernel<DT, FMT>, j.first[3], st, j);
   STRATA_D(STRATA_DTYPE_F32, STRATA_MX_FP4)
   STRATA_D(STRATA_DTYPE_F16, STRATA_MX_FP4)
   STRATA_D(STRATA_DTYPE_BF16, STRATA_MX_FP4)
@@ -276,7 +318,7 @@ cudaError_t launch_mx_dequantize(const MxDequantArgs& a, cudaStream_t st) {
 cudaError_t launch_mx_tile_scales(const uint8_t* src, int64_t rows, int64_t K, uint8_t* dst,
                                   cudaStream_t st) {
   const uint64_t words = (uint64_t)mx_scale_plane(rows, K, STRATA_MX_TILES) / 4;
-  return launch_groups(mx_tile_scales_kernel, words, (uint64_t)kQThreads, st, src, rows,
+  return launch_blocks(mx_tile_scales_kernel, (words + kQThreads - 1) / kQThreads, st, src, rows,
                        (int)(K / kMxBlock), (int)mx_ceil(K, 128), words,
                        reinterpret_cast<uint32_t*>(dst));
 }

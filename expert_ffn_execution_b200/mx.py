@@ -268,44 +268,33 @@ def mx_linear(x: MXTensor, w: MXTensor, bias: torch.Tensor | None = None,
     return out
 
 
-def _blob_planes(H: int, I: int):
-    """(codes offset, scales offset, rows, K) of gate, up and down in an MXFP4
-    expert blob: each plane on a 256-byte boundary."""
-    off, planes = 0, []
-    for rows, K in ((I, H), (I, H), (H, I)):
-        codes = off
-        off = (off + rows * K // 2 + 255) & ~255
-        planes.append((codes, off, rows, K))
-        off = (off + rows * K // 32 + 255) & ~255
-    return planes
-
-
 def pack_experts(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
                  stream=None) -> ExpertWeights:
-    """Quantises E experts' weights, gate and up [E, I, H], down [E, H, I], to
-    the MXFP4 blobs that moe_experts reads."""
+    """Quantises E experts' weights, gate and up [E, I, H], down [E, H, I], all
+    of one dtype, to the MXFP4 blobs that moe_experts reads."""
     if gate.dim() != 3 or up.shape != gate.shape:
         raise ValueError("gate and up must be [E, I, H]")
     E, I, H = gate.shape
     if down.shape != (E, H, I) or H % 128 or I % 128 or not gate.numel():
         raise ValueError("down must be [E, H, I], H and I positive multiples of 128")
     ws = (gate, up, down)
+    dt, dev, el = _dtype(gate.dtype), _device(*ws), gate.element_size()
+    rows, experts = [], []
     for w in ws:
-        if w.stride(2) != 1 or any(w.stride(i) * w.element_size() % 16 for i in (0, 1)) or \
-                w.data_ptr() % 16:
+        expert, row, step = w.stride()
+        if w.dtype != gate.dtype:
+            raise TypeError("gate, up and down must have one dtype")
+        if step != 1 or row * el % 16 or (E > 1 and expert * el % 16) or w.data_ptr() % 16:
             raise ValueError("weights must have contiguous rows that start on 16-byte boundaries")
-    dts, dev = [_dtype(w.dtype) for w in ws], _device(*ws)
+        rows.append(row)
+        experts.append(expert)
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return pack_experts(gate, up, down, stream)
-    lib, stream = _enter(dev, stream)
-    size = B.strata_expert_bytes(B.FMT_MXFP4_32, H, I)
-    blobs = torch.empty(E, size, dtype=torch.uint8, device=dev)
-    at = blobs.data_ptr()
-    for w, dt, (c, s, rows, K) in zip(ws, dts, _blob_planes(H, I)):
-        rc = lib.moe_mx_quantize(w.data_ptr(), dt, E, rows, K, w.stride(1), w.stride(0), B.MX_FP4,
-                                 at + c, size, at + s, B.MX_ROWS, size, stream)
-        _check("moe_mx_quantize", rc)
+    _, stream = _enter(dev, stream)
+    blobs = torch.empty(E, B.strata_expert_bytes(B.FMT_MXFP4_32, H, I), dtype=torch.uint8, device=dev)
+    B.moe_mx_pack_experts(gate, up, down, dt, rows, experts, E, H, I, blobs, blobs.stride(0),
+                          stream)
     return ExpertWeights(blobs, B.FMT_MXFP4_32, H, I)
 
 
@@ -313,17 +302,13 @@ def unpack_experts(w: ExpertWeights, dtype=torch.float32, stream=None):
     """(gate, up, down) that MXFP4 blobs stand for: [E, I, H] twice, [E, H, I]."""
     if w.fmt != B.FMT_MXFP4_32:
         raise ValueError("only MXFP4 blobs are read back")
-    dt, dev, E = _dtype(dtype), _device(w.blobs), w.num_experts
+    dt, dev, E, H, I = _dtype(dtype), _device(w.blobs), w.num_experts, w.hidden, w.inter
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return unpack_experts(w, dtype, stream)
-    lib, stream = _enter(dev, stream)
-    at, size = w.blobs.data_ptr(), w.blobs.stride(0)
-    outs = []
-    for c, s, rows, K in _blob_planes(w.hidden, w.inter):
-        o = torch.empty(E, rows, K, dtype=dtype, device=dev)
-        rc = lib.moe_mx_dequantize(at + c, size, at + s, B.MX_ROWS, size, B.MX_FP4, E, rows, K,
-                                   o.data_ptr(), dt, K, rows * K, stream)
-        _check("moe_mx_dequantize", rc)
-        outs.append(o)
-    return tuple(outs)
+    _, stream = _enter(dev, stream)
+    gate = torch.empty(E, I, H, dtype=dtype, device=dev)
+    up = torch.empty(E, I, H, dtype=dtype, device=dev)
+    down = torch.empty(E, H, I, dtype=dtype, device=dev)
+    B.moe_mx_unpack_experts(w.blobs, w.blobs.stride(0), E, H, I, gate, up, down, dt, stream)
+    return gate, up, down

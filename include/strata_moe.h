@@ -428,6 +428,25 @@ STRATA_API int32_t moe_mx_dequantize(const void* codes, uint64_t codes_batch_str
                           int32_t dst_dtype, int64_t dst_row_stride, int64_t dst_batch_stride,
                           void* stream);
 
+/* E experts' weights -> STRATA_FMT_MXFP4_32 blobs as moe_experts reads them,
+ * and back: moe_mx_quantize / moe_mx_dequantize on the three planes of every
+ * blob in one launch.
+ *   gate, up [E,I,H], down [E,H,I] of dtype F32 / F16 / BF16; row_strides and
+ *   expert_strides: HOST arrays of three (gate, up, down), in elements, as
+ *   src_row_stride and src_batch_stride above; the results of
+ *   moe_mx_unpack_experts are contiguous
+ *   blobs  256-byte aligned, blob_stride a multiple of 256 and at least
+ *          strata_expert_bytes(STRATA_FMT_MXFP4_32, H, I); bytes between the
+ *          planes and behind a blob's last are not written
+ * Limits: H, I multiples of 128; E >= 0 (0: no-op). */
+STRATA_API int32_t moe_mx_pack_experts(const void* gate, const void* up, const void* down,
+                            int32_t dtype, const int64_t* row_strides,
+                            const int64_t* expert_strides, int32_t E, int32_t H, int32_t I,
+                            void* blobs, uint64_t blob_stride, void* stream);
+STRATA_API int32_t moe_mx_unpack_experts(const void* blobs, uint64_t blob_stride, int32_t E, int32_t H,
+                              int32_t I, void* gate, void* up, void* down, int32_t dtype,
+                              void* stream);
+
 /* Scales from STRATA_MX_ROWS to STRATA_MX_TILES (both of one [rows, K]
  * matrix): what a checkpoint's scales need once before moe_mx_linear reads
  * them.  tiles 16-byte aligned, moe_mx_scale_bytes() bytes; rows == 0 is a

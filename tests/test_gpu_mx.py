@@ -296,19 +296,20 @@ def test_linear_is_exact_on_small_integers(T, xf, wf):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
-@pytest.mark.parametrize("T,N", [(5, 300), (150, 259)])
+@pytest.mark.parametrize("T,N", [(5, 300), (150, 259), (1100, 2050), (1100, 2047), (1030, 2176)])
 def test_linear_bias_dtypes_and_row_stride(T, N, dtype):
     K = 512
     x, xv = random_mx(T, K, sm.MX_FP8, 1, 118, 122)
     w, wv = random_mx(N, K, sm.MX_FP4, 2, 118, 122)
     bias = torch.randn(N, device=DEV, generator=gen(3))
-    wide = torch.full((T + 2, N + 13), 7.0, dtype=dtype, device=DEV)
-    out = wide[1:-1, 3:N + 3]
-    got = sm.mx_linear(x, w, bias, out=out)
-    assert got is out
-    assert_product(out, xv, wv, bias)
-    wide[1:-1, 3:N + 3] = 7.0
-    assert (wide == 7.0).all()  # nothing else was written
+    for extra, at in ((13, 3), (14, 2), (32, 8)):  # rows on odd, 4-byte and 16-byte boundaries
+        wide = torch.full((T + 2, (N + extra + 15) // 16 * 16 + extra % 16), 7.0, dtype=dtype, device=DEV)
+        out = wide[1:-1, at:N + at]
+        got = sm.mx_linear(x, w, bias, out=out)
+        assert got is out
+        assert_product(out, xv, wv, bias)
+        wide[1:-1, at:N + at] = 7.0
+        assert (wide == 7.0).all()  # nothing else was written
 
 
 @pytest.mark.parametrize("xf,wf", PAIRS)
@@ -429,15 +430,36 @@ def test_packed_experts_in_the_layer(T):
     assert_product(y, n.mx.dequantize().double(), wv)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("E,I,H", [(1, 128, 128), (5, 128, 384), (3, 640, 2560)])
-def test_pack_experts_strides(E, I, H):
+def test_pack_experts_strides(E, I, H, dtype):
     """Weights whose experts or rows are further apart than they are long."""
     g = gen(50)
-    gate = torch.randn(E, I, H + 16, device=DEV, generator=g).half()[:, :, 8:H + 8]
-    up = torch.randn(2 * E, I, H, device=DEV, generator=g)[::2]
-    down = torch.randn(E, H, I, device=DEV, generator=g).bfloat16()
+    gate = torch.randn(E, I, H + 16, device=DEV, generator=g).to(dtype)[:, :, 8:H + 8]
+    up = torch.randn(2 * E, I, H, device=DEV, generator=g).to(dtype)[::2]
+    down = torch.randn(E, H, I, device=DEV, generator=g).to(dtype)
     blob = sm.pack_experts(gate, up, down)
     assert blob.blobs.shape == (E, sm.strata_expert_bytes(sm.FMT_MXFP4_32, H, I))
     for t, v in zip((gate, up, down), blob.dequantize(torch.bfloat16)):
         c, s = ref.quantize(n64(t).reshape(-1, t.shape[2]), sm.MX_FP4)
         assert np.array_equal(n64(v).reshape(c.shape), ref.dequantize(c, s, sm.MX_FP4))
+
+
+def test_pack_experts_leaves_the_rest():
+    """Blobs further apart than they are long keep the bytes between them."""
+    E, I, H = 3, 128, 128
+    size = sm.strata_expert_bytes(sm.FMT_MXFP4_32, H, I)
+    ws = [torch.randn(E, r, k, device=DEV, generator=gen(60 + i)) for i, (r, k) in enumerate(((I, H), (I, H), (H, I)))]
+    blobs = torch.full((E, size + 512), 0xA5, dtype=torch.uint8, device=DEV)
+    sm.moe_mx_pack_experts(*ws, sm.DTYPE_F32, [w.stride(1) for w in ws], [w.stride(0) for w in ws], E, H, I, blobs,
+                           size + 512)
+    assert (blobs[:, size:] == 0xA5).all()
+    want = sm.pack_experts(*ws).blobs
+    planes = torch.zeros(size, dtype=torch.bool)
+    at = 0
+    for r, k in ((I, H), (I, H), (H, I)):
+        for n in (r * k // 2, r * k // 32):
+            planes[at:at + n] = True
+            at = (at + n + 255) // 256 * 256
+    assert torch.equal(blobs[:, :size].cpu()[:, planes], want.cpu()[:, planes])
+    assert (blobs[:, :size].cpu()[:, ~planes] == 0xA5).all()

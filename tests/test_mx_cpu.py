@@ -92,6 +92,37 @@ def test_tile_scales_refuses():
         assert sm.moe_mx_tile_scales(*a, stream=0, check=False) == B.EINVAL
 
 
+def pack(**k):
+    a = dict(gate=P, up=P, down=P, dtype=sm.DTYPE_BF16, row_strides=(256, 256, 128),
+             expert_strides=(1 << 15,) * 3, E=2, H=256, I=128, blobs=P, blob_stride=1 << 20)
+    a.update(k)
+    return sm.moe_mx_pack_experts(**a, stream=0, check=False)
+
+
+def unpack(**k):
+    a = dict(blobs=P, blob_stride=1 << 20, E=2, H=256, I=128, gate=P, up=P, down=P,
+             dtype=sm.DTYPE_BF16)
+    a.update(k)
+    return sm.moe_mx_unpack_experts(**a, stream=0, check=False)
+
+
+BAD_EXPERTS = [dict(gate=None), dict(up=P + 2), dict(down=None), dict(dtype=5), dict(E=-1), dict(H=192),
+               dict(I=0), dict(blobs=None), dict(blobs=P + 128), dict(blob_stride=(1 << 20) + 64),
+               dict(blob_stride=256)]
+
+
+@pytest.mark.parametrize("k", BAD_EXPERTS + [
+    dict(row_strides=None), dict(expert_strides=None), dict(row_strides=(260, 256, 128)),
+    dict(row_strides=(256, -256, 128)), dict(expert_strides=(1 << 15, 1 << 15, 9))], ids=str)
+def test_pack_experts_refuses(k):
+    assert pack(**k) == B.EINVAL
+
+
+@pytest.mark.parametrize("k", BAD_EXPERTS, ids=str)
+def test_unpack_experts_refuses(k):
+    assert unpack(**k) == B.EINVAL
+
+
 def norm(**k):
     a = dict(x=P, x_dtype=0, delta=P, delta_dtype=2, gain=P, T=4, H=64, eps=1e-6, residual_out=P,
              out=P, out_dtype=2, mx_fmt=sm.MX_FP8, codes=P, scales=P, scale_layout=sm.MX_TILES)
@@ -135,6 +166,8 @@ def test_empty_is_a_noop():
     assert quant(batch=0, src=None, codes=None, scales=None) == B.OK
     assert dequant(rows=0, dst=None, codes=None, scales=None) == B.OK
     assert sm.moe_mx_tile_scales(None, 0, 64, None, stream=0, check=False) == B.OK
+    assert pack(E=0, gate=None, blobs=None) == B.OK
+    assert unpack(E=0, gate=None, blobs=None) == B.OK
     assert norm(T=0, x=None) == B.OK
     assert linear(T=0, x_codes=None, y=None) == B.OK
 
@@ -180,3 +213,6 @@ def test_torch_level_refusals():
         sm.pack_experts(w, w, w)
     with pytest.raises(ValueError, match="gate"):
         sm.pack_experts(w, w[:1], w)
+    e = sm.ExpertWeights(torch.zeros(2, 1 << 17, dtype=torch.uint8), sm.FMT_Q2_32, 256, 128)
+    with pytest.raises(ValueError, match="MXFP4"):
+        e.dequantize()
