@@ -43,8 +43,9 @@ struct GemmCfg {
   static constexpr int stage = AB + BB + SA + SBb;
   static constexpr int stride = (stage + 1023) / 1024 * 1024;
   static constexpr int epi = kGEpi * 32 * (ANY ? 4 * kGPitch : 64);
-  static constexpr int S = (227 * 1024 - 2048 - epi) / stride;
-  static constexpr int smem = S * stride + epi + 2048;
+  static constexpr int bias = kGEpi * 128 * 4;
+  static constexpr int S = (227 * 1024 - 2048 - epi - bias) / stride;
+  static constexpr int smem = S * stride + epi + bias + 2048;
   static constexpr int sfcols = 12 * ST;
   static_assert(kGN + S * sfcols <= 512, "sums and scales fit the tensor memory");
 };
@@ -144,7 +145,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* epi = smem + C::S * C::stride;
-  uint64_t* full = reinterpret_cast<uint64_t*>(epi + C::epi);
+  float* bias_s = reinterpret_cast<float*>(epi + C::epi);
+  uint64_t* full = reinterpret_cast<uint64_t*>(bias_s + C::bias / 4);
   uint64_t* empty = full + C::S;
   uint64_t* tfull = empty + C::S;
   uint64_t* tempty = tfull + 1;
@@ -266,6 +268,14 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     for (int tile = pair; tile < tiles; tile += pairs, ++it) {
       const int t0 = (tile % mt) * kGM + 128 * (int)rank + 32 * q;
       const int n0 = (tile / mt) * kGN + 128 * half;
+      float* const bs = bias_s + warp * 128;
+      if (a.bias) {  // this warp's 128 features' while the MMAs run
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = n0 + 32 * i + lane;
+          bs[32 * i + lane] = n < a.N ? a.bias[n] : 0.f;
+        }
+      }
       const bool ok = mbar_wait_guarded(tfull, it & 1, a.status, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
@@ -279,8 +289,13 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       if (lane == 0) mbar_arrive_cluster(lead);
       if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (n0 + i < a.N) r[i] = __float_as_uint(__uint_as_float(r[i]) + a.bias[n0 + i]);
+        for (int i = 0; i < 32; ++i) {
+          const float4 b = reinterpret_cast<const float4*>(bs)[i];
+          r[4 * i] = __float_as_uint(__uint_as_float(r[4 * i]) + b.x);
+          r[4 * i + 1] = __float_as_uint(__uint_as_float(r[4 * i + 1]) + b.y);
+          r[4 * i + 2] = __float_as_uint(__uint_as_float(r[4 * i + 2]) + b.z);
+          r[4 * i + 3] = __float_as_uint(__uint_as_float(r[4 * i + 3]) + b.w);
+        }
       }
       if constexpr (kEl == 2) {
 #pragma unroll
