@@ -275,13 +275,22 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     tc_fence_before();
   }
   __syncthreads();
-  if (*abort_flag && threadIdx.x == 0) {
+  if (*abort_flag) {  // the same for all threads: every guarded wait is behind them
     // a wait gave up: every copy that was started lands, and every MMA ends,
     // before the shared and tensor memory are released (bounded)
-    const int n = *issued;
-    for (int s = 0; s < S && s < n; ++s)
-      mbar_wait_bounded(&full[s], last_armed_parity(n, S, s), a.status, kLDrainCycles);
-    mbar_wait_bounded(tfull, 0, a.status, kLDrainCycles);
+    if (threadIdx.x == 0) {
+      const int n = *issued;
+      for (int s = 0; s < S && s < n; ++s)
+        mbar_wait_bounded(&full[s], last_armed_parity(n, S, s), a.status, kLDrainCycles);
+      mbar_wait_bounded(tfull, 0, a.status, kLDrainCycles);
+    }
+    __syncthreads();
+  }
+  // Tensor memory goes before the other ranks are waited for: a rank that is
+  // itself waiting for tensor memory (another kernel's CTA has it) holds none.
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tbase, C::cols(S));
   }
   __syncwarp();
   const uint8_t* sums = smem;
@@ -312,10 +321,6 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
   }
   __syncwarp();
   if (splits > 1) cluster_sync_relaxed();  // nobody leaves while its sums are being sent
-  if (warp == 5) {
-    tc_fence_after();
-    tmem_dealloc(tbase, C::cols(S));
-  }
 }
 
 // Codes of a matrix as 128-byte (shared memory) x `box_rows` boxes.

@@ -77,8 +77,9 @@ def _scale_bytes(rows: int, K: int, layout: int) -> int:
 def _check_format(fmt, rows, K, layout):
     if fmt not in (B.MX_FP4, B.MX_FP8) or layout not in (B.MX_ROWS, B.MX_TILES):
         raise ValueError("fmt must be MX_FP4 or MX_FP8, layout MX_ROWS or MX_TILES")
-    if rows < 0 or K < 32 or K % 32:
-        raise ValueError(f"rows = {rows}, K = {K}: rows >= 0 and K a positive multiple of 32 are wanted")
+    if not 0 <= rows < 1 << 31 or not 32 <= K < 1 << 31 or K % 32:
+        raise ValueError(f"rows = {rows}, K = {K}: rows >= 0 and K a positive multiple of 32, "
+                         "both below 2^31, are wanted")
 
 
 class MXTensor:
@@ -201,6 +202,8 @@ def add_rmsnorm(x: torch.Tensor, delta: torch.Tensor | None = None,
     h as out_dtype (None: not written) and as microscaled `fmt` (0: not
     written).  r goes to residual_out (x for in place) or a new tensor."""
     shape = x.shape
+    if len(shape) != 2 or shape[0] >= 1 << 31 or shape[1] >= 1 << 31:
+        raise ValueError(f"x must be a matrix [T, H] of sizes below 2^31, got {tuple(shape)}")
     T, H = shape
     for t, what in ((x, "x"), (delta, "delta"), (residual_out, "residual_out")):
         if t is not None and (t.shape != shape or not t.is_contiguous()):

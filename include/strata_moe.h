@@ -480,7 +480,9 @@ STRATA_API int32_t moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* d
  *   (x_fmt, w_fmt): (FP4, FP4), (FP8, FP4), (FP8, FP8); (FP4, FP8) returns
  *      STRATA_EUNSUPPORTED
  *   dev_status may be NULL.
- * A row of x or w with a NaN block gives NaN in its outputs.  The sums'
+ * A row of x or w with a NaN block or code gives NaN in its outputs; products
+ * beyond fp32's range become infinite, those below it may vanish.  y overlaps
+ * no input.  The sums'
  * order depends on (T, N, K), the formats and the device alone: the same
  * bits on every run.  No workspace.
  * Limits: T >= 0 (0: no-op) up to 2^22, N >= 1, K a multiple of 128, at least

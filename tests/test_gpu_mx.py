@@ -352,6 +352,41 @@ def test_linear_nothing():
     assert sm.mx_linear(x, w).shape == (0, 64)
 
 
+@pytest.mark.parametrize("xf,wf", PAIRS)
+def test_linear_tiles_that_start_inside_a_scale_tile(xf, wf):
+    """Two tiles of 64 tokens in one tile of scales, every row's scales its own."""
+    for T, N, K in ((128, 256, 2048), (100, 512, 1024), (192, 384, 1024)):
+        x, xv = random_mx(T, K, xf, T, 110, 140)
+        w, wv = random_mx(N, K, wf, T + 1)
+        assert_product(sm.mx_linear(x, w, out_dtype=torch.float32), xv, wv)
+
+
+def test_linear_on_two_streams_at_once():
+    """Calls of every form (split and not, single CTAs and pairs) side by side
+    on two streams give the bits of the calls in turn."""
+    cases = [(4, 2560, 2560), (600, 4000, 512), (64, 1024, 4096), (128, 4096, 1024), (1, 12000, 768)]
+    made = []
+    for i, (T, N, K) in enumerate(cases):
+        x, w = (sm.mx_quantize(torch.randn(r, K, device=DEV, generator=gen(70 + 2 * i + j)), f)
+                for j, (r, f) in enumerate(((T, sm.MX_FP8), (N, sm.MX_FP4))))
+        made.append((x, w, sm.mx_linear(x, w, out_dtype=torch.float32)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for i, (x, w, want) in enumerate(made):
+            for s in streams:
+                with torch.cuda.stream(s):
+                    got.append((sm.mx_linear(x, w, out_dtype=torch.float32, dev_status=status), want))
+        made.append(made.pop(0))  # another neighbour each time
+    torch.cuda.synchronize()
+    assert sm.strata_read_status(status) == 0
+    for y, want in got:
+        assert torch.equal(y, want)
+
+
 # ---------------------------------------------------------------- together
 def step(x, d, gain, w, out):
     n = sm.add_rmsnorm(x, d, gain, fmt=sm.MX_FP8, residual_out=x)
