@@ -1,7 +1,8 @@
 """Builds libstrata_moe.so in-tree with nvcc for sm_100a.
 
 Each .cu under csrc/ is compiled to an object (in parallel) and linked into one
-shared library next to this file.  Run `python -m expert_ffn_execution_b200.build`.
+shared library next to this file; native/mxcalls.cpp becomes the Python module
+_mxcalls beside it (g++, the CPython headers).  Run `python -m expert_ffn_execution_b200.build`.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libstrata_moe.so")
+CALLS_SRC = os.path.join(HERE, "native", "mxcalls.cpp")
+CALLS = os.path.join(HERE, "_mxcalls.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -53,7 +57,23 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_calls(force: bool = False) -> str:
+    deps = (CALLS_SRC, os.path.join(INCLUDE, "strata_moe.h"))
+    if not force and os.path.exists(CALLS) and all(
+            os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
+        return CALLS
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-Wall", "-shared", "-fPIC",
+           "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, CALLS_SRC,
+           "-o", CALLS + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stderr}")
+    os.replace(CALLS + ".tmp", CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_calls(force)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

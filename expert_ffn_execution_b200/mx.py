@@ -1,17 +1,21 @@
 """Torch-level calls of the microscaled operators: they check shapes, types and
 devices, allocate the outputs and call the library on the tensors' device and
-that device's current stream (or `stream`).  No arithmetic happens here.
+that device's current stream (or `stream`).  No arithmetic happens here, and
+nothing is recorded for a backward pass.
 
 A tensor that is used on another stream than the one it was made on is the
 caller's to order and to keep alive, as with any asynchronous call.
 
 A decode step's kernels take a few microseconds, so the host's part of a call
-counts: the library's functions are called directly, the current stream is
-read as a raw handle, the codes and scales that a call makes share one
-allocation, and their tensors are made when they are asked for.
+counts.  The codes and scales that a call makes share one allocation, their
+tensors are made when they are asked for, and calls that need nothing from
+this file but its checks are made by native/mxcalls.cpp (quantising 4 rows: 8.4
+us here, 5.9 us there); it returns None for every other call, which then runs
+here.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple
 
 import torch
@@ -19,7 +23,28 @@ import torch
 from . import _binding as B
 from .layer import ExpertWeights
 
+try:
+    from . import _mxcalls
+except ImportError:  # not built: every call runs here
+    _mxcalls = None
+
 _DTYPES = {torch.float32: B.DTYPE_F32, torch.float16: B.DTYPE_F16, torch.bfloat16: B.DTYPE_BF16}
+_fast = None  # _mxcalls, once it has been given the library
+
+
+def _library():
+    """The loaded library; the first call arms the native one."""
+    global _fast
+    lib = B._lib or B.load()
+    if _fast is None and _mxcalls is not None:
+        names = ("moe_mx_quantize", "moe_mx_dequantize", "moe_add_rmsnorm", "moe_mx_linear")
+        _mxcalls.setup(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+                       torch.empty, torch.Tensor, torch.nn.Parameter, torch.device,
+                       torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream,
+                       (torch.float32, torch.float16, torch.bfloat16, torch.uint8, torch.int32),
+                       MXTensor, AddNorm)
+        _fast = _mxcalls
+    return lib
 
 
 def _dtype(dtype) -> int:
@@ -47,7 +72,7 @@ def _enter(dev, stream):
         stream = torch._C._cuda_getCurrentRawStream(dev.index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    return B._lib or B.load(), stream
+    return _library(), stream
 
 
 def _elsewhere(dev) -> bool:
@@ -82,13 +107,21 @@ def _check_format(fmt, rows, K, layout):
                          "both below 2^31, are wanted")
 
 
-class MXTensor:
+_FIELDS = ("fmt", "layout", "rows", "K", "codes_ptr", "scales_ptr", "index", "device", "_both",
+           "_codes", "_scales")
+if _mxcalls is not None:
+    _Matrix = _mxcalls.Matrix  # these fields, natively
+else:
+    class _Matrix:
+        __slots__ = _FIELDS
+
+
+class MXTensor(_Matrix):
     """A microscaled matrix [rows, K] on the device: uint8 codes [rows, K/2]
     (MX_FP4) or [rows, K] (MX_FP8) and uint8 scales, [rows, K/32] (MX_ROWS) or
     the flat plane of tiles that mx_linear reads (MX_TILES)."""
 
-    __slots__ = ("fmt", "rows", "K", "layout", "device", "codes_ptr", "scales_ptr", "_codes",
-                 "_scales", "_both")
+    __slots__ = ()
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: int, rows: int, K: int,
                  layout: int):
@@ -97,7 +130,7 @@ class MXTensor:
                            (scales, _scale_bytes(rows, K, layout), "scales")):
             if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"{what} must be contiguous uint8 of {n} bytes")
-        self.device = codes.device
+        self.device, self.index = codes.device, codes.get_device()
         if scales.device != self.device:
             raise ValueError(f"codes on {self.device} and scales on {scales.device}")
         self.fmt, self.rows, self.K, self.layout = fmt, rows, K, layout
@@ -109,7 +142,8 @@ class MXTensor:
         """One to be written by a call: both planes in one allocation."""
         _check_format(fmt, rows, K, layout)
         q = cls.__new__(cls)
-        q.fmt, q.rows, q.K, q.layout, q.device = fmt, rows, K, layout, dev
+        q.fmt, q.rows, q.K, q.layout = fmt, rows, K, layout
+        q.device, q.index = dev, dev.index
         at = (_code_bytes(rows, fmt, K) + 255) & ~255
         q._both = torch.empty(at + _scale_bytes(rows, K, layout), dtype=torch.uint8, device=dev)
         q._codes = q._scales = None
@@ -134,6 +168,8 @@ class MXTensor:
 
     def dequantize(self, dtype=torch.float32, stream=None) -> torch.Tensor:
         """The matrix's values: [rows, K] of `dtype`."""
+        if _fast and (out := _fast.dequantize(self, dtype, stream)) is not None:
+            return out
         dt, dev = _dtype(dtype), _device(self)
         if _elsewhere(dev):
             with torch.cuda.device(dev):
@@ -149,6 +185,8 @@ class MXTensor:
 def mx_quantize(x: torch.Tensor, fmt: int, layout: int = B.MX_TILES, stream=None) -> MXTensor:
     """x [rows, K] in the microscaled format `fmt`.  Rows may be further apart
     than they are long; other strides are refused, not copied."""
+    if _fast and (q := _fast.quantize(x, fmt, layout, stream)) is not None:
+        return q
     if x.dim() != 2:
         raise ValueError(f"x must be a matrix, got shape {tuple(x.shape)}")
     rows, K = x.shape
@@ -201,6 +239,9 @@ def add_rmsnorm(x: torch.Tensor, delta: torch.Tensor | None = None,
     """r = x + delta; h = r / sqrt(mean r^2 + eps) * gain, per row of x [T, H];
     h as out_dtype (None: not written) and as microscaled `fmt` (0: not
     written).  r goes to residual_out (x for in place) or a new tensor."""
+    if _fast and (n := _fast.add_rmsnorm(x, delta, gain, eps, out_dtype, fmt, layout, residual_out,
+                                         stream)) is not None:
+        return n
     shape = x.shape
     if len(shape) != 2 or shape[0] >= 1 << 31 or shape[1] >= 1 << 31:
         raise ValueError(f"x must be a matrix [T, H] of sizes below 2^31, got {tuple(shape)}")
@@ -239,6 +280,8 @@ def mx_linear(x: MXTensor, w: MXTensor, bias: torch.Tensor | None = None,
               dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """x [T, K] times w [N, K] transposed, plus bias [N]: [T, N] of out_dtype
     (or of `out`, whose rows may be further apart than N)."""
+    if _fast and (y := _fast.linear(x, w, bias, out_dtype, out, dev_status, stream)) is not None:
+        return y
     T, N, K = x.rows, w.rows, w.K
     if x.K != K:
         raise ValueError(f"x has K = {x.K}, w K = {K}")

@@ -3,6 +3,9 @@
 Quantised codes and scales, and values read back, are compared bit for bit:
 the format determines them.  Tolerances elsewhere are counted in half steps
 (2^-8 for bf16, 2^-11 for fp16, 2^-24 for fp32) as each test derives."""
+import gc
+import sys
+
 import numpy as np
 import pytest
 
@@ -12,6 +15,7 @@ if not torch.cuda.is_available():
 
 import expert_ffn_execution_b200 as sm  # noqa: E402
 import oracle  # noqa: E402
+from expert_ffn_execution_b200 import mx  # noqa: E402
 from tests import mx_reference as ref  # noqa: E402
 from tests.harness import OUT_REL_L2, check_routing, rel_l2_rows  # noqa: E402
 
@@ -65,6 +69,13 @@ def assert_quantised(q, x):
     else:
         assert np.array_equal(s, scales)
     assert np.array_equal(host_codes(q), codes)
+
+
+@pytest.fixture(autouse=True, scope="module")
+def armed():
+    """The native calls are those that run."""
+    sm.mx_quantize(torch.zeros(1, 32, device=DEV), sm.MX_FP8)
+    assert mx._fast is not None
 
 
 # ---------------------------------------------------------------- quantiser
@@ -498,3 +509,88 @@ def test_pack_experts_leaves_the_rest():
             at = (at + n + 255) // 256 * 256
     assert torch.equal(blobs[:, :size].cpu()[:, planes], want.cpu()[:, planes])
     assert (blobs[:, :size].cpu()[:, ~planes] == 0xA5).all()
+
+
+# ---------------------------------------------------------------- the native calls
+def every_call(x, d, gain, w, bias):
+    n = sm.add_rmsnorm(x, d, gain, 1e-5, out_dtype=torch.bfloat16, fmt=sm.MX_FP8)
+    p = sm.add_rmsnorm(x, gain=gain, fmt=sm.MX_FP4, layout=sm.MX_ROWS)
+    r = x.clone()
+    q = sm.add_rmsnorm(r, d, out_dtype=torch.float32, residual_out=r)
+    out = torch.empty(x.shape[0], w.rows + 8, dtype=torch.float16, device=DEV)[:, :w.rows]
+    z = sm.mx_quantize(x, sm.MX_FP8)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    return (n.residual, n.out, n.mx.codes, n.mx.scales, p.mx.codes, p.mx.scales, q.residual, q.out,
+            p.mx.dequantize(torch.float16), z.codes, z.scales, sm.mx_linear(n.mx, w),
+            sm.mx_linear(z, w, bias, torch.float32, dev_status=status), sm.mx_linear(z, w, bias, out=out).clone())
+
+
+def test_native_calls_are_the_python_ones(monkeypatch):
+    g = gen(80)
+    x = torch.randn(5, 256, device=DEV, generator=g)
+    args = (x, torch.randn(5, 256, device=DEV, generator=g).half(), 1 + torch.rand(256, device=DEV, generator=g),
+            sm.mx_quantize(torch.randn(70, 256, device=DEV, generator=g), sm.MX_FP4),
+            torch.randn(70, device=DEV, generator=g))
+    native = every_call(*args)
+    as_parameters = every_call(args[0], args[1], torch.nn.Parameter(args[2]), *args[3:])
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        aside = every_call(*args)
+        torch.cuda.synchronize()
+    monkeypatch.setattr(mx, "_fast", None)
+    monkeypatch.setattr(mx, "_mxcalls", None)
+    for got in (native, as_parameters, aside):
+        for a, b in zip(got, every_call(*args)):
+            assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
+
+
+def test_native_calls_keep_nothing():
+    x = torch.randn(64, 256, device=DEV)
+    d = torch.randn(64, 256, device=DEV)
+    w = sm.mx_quantize(torch.randn(128, 256, device=DEV), sm.MX_FP4)
+    b = torch.randn(128, device=DEV)
+    held = [sys.getrefcount(o) for o in (x, d, w, b, torch.float32, x.device, sm.MXTensor)]
+    for _ in range(3):
+        every_call(x, d, None, w, b)
+    torch.cuda.synchronize()
+    gc.collect()
+    used = torch.cuda.memory_allocated()
+    for _ in range(50):
+        every_call(x, d, None, w, b)
+    gc.collect()
+    assert torch.cuda.memory_allocated() == used
+    for before, o in zip(held, (x, d, w, b, torch.float32, x.device, sm.MXTensor)):
+        assert sys.getrefcount(o) <= before + 2
+
+
+def test_native_calls_leave_refusals_to_python():
+    """The messages of mx.py, with the native calls armed."""
+    x = torch.zeros(4, 128, device=DEV)
+    q = sm.mx_quantize(x, sm.MX_FP8)
+    rows = sm.mx_quantize(x, sm.MX_FP8, sm.MX_ROWS)
+    w4 = sm.mx_quantize(x, sm.MX_FP4)
+    for call, error, match in (
+            (lambda: sm.mx_quantize(x.T, sm.MX_FP8), ValueError, "rows"),
+            (lambda: sm.mx_quantize(x[:, 1:97], sm.MX_FP8), ValueError, "16-byte"),
+            (lambda: sm.mx_quantize(x[:, :48], sm.MX_FP8), ValueError, "multiple of 32"),
+            (lambda: sm.mx_quantize(x.double(), sm.MX_FP8), TypeError, "dtype"),
+            (lambda: sm.mx_quantize(x.cpu(), sm.MX_FP8), ValueError, "CUDA"),
+            (lambda: sm.mx_quantize(x, 7), ValueError, "fmt"),
+            (lambda: sm.mx_quantize(x, sm.MX_FP8, 7), ValueError, "layout"),
+            (lambda: sm.mx_quantize(x[0], sm.MX_FP8), ValueError, "matrix"),
+            (lambda: q.dequantize(torch.int32), TypeError, "dtype"),
+            (lambda: sm.add_rmsnorm(x, x.cpu(), fmt=sm.MX_FP8), ValueError, "on c"),
+            (lambda: sm.add_rmsnorm(x, x[:2], fmt=sm.MX_FP8), ValueError, "delta"),
+            (lambda: sm.add_rmsnorm(x, gain=x[0].half(), fmt=sm.MX_FP8), ValueError, "gain"),
+            (lambda: sm.add_rmsnorm(x), ValueError, "out_dtype"),
+            (lambda: sm.add_rmsnorm(x, eps=-1.0, fmt=sm.MX_FP8), sm.StrataError, "invalid"),
+            (lambda: sm.add_rmsnorm(x, residual_out=x.half(), fmt=sm.MX_FP8), TypeError, "residual_out"),
+            (lambda: sm.mx_linear(rows, q), ValueError, "tiles"),
+            (lambda: sm.mx_linear(q, sm.mx_quantize(x[:, :64], sm.MX_FP8)), ValueError, "K = "),
+            (lambda: sm.mx_linear(w4, q), sm.StrataError, "unsupported"),
+            (lambda: sm.mx_linear(q, q, x[0]), ValueError, "bias"),
+            (lambda: sm.mx_linear(q, q, out=x), ValueError, "out"),
+            (lambda: sm.mx_linear(q, q, dev_status=x), ValueError, "dev_status"),
+            (lambda: sm.mx_linear(q, q, out_dtype=torch.int32), TypeError, "dtype")):
+        with pytest.raises(error, match=match):
+            call()
