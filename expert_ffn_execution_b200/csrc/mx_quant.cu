@@ -9,7 +9,7 @@
 // Matrix, row and column of the first come from its flat index by division,
 // those of the next, and their offsets, by adding.  8192 x 4096 bf16 to FP8:
 // 36 us with 8 elements and three divisions a piece, 24 us without the
-// divisions, 18 us with 16 elements and added offsets.
+// divisions, 18 us (5.7 TB/s) with 16 elements and added offsets.
 #include "mx.cuh"
 #include "tc05.cuh"
 
@@ -109,8 +109,8 @@ struct Jobs {
   Stride src[3], dst[3];
   uint32_t first[4];
 };
-// MANY: more than one batch (one alone is found at compile time: 23.3 us for
-// 25.7, 52M bf16 to MXFP4).
+// MANY: more than one batch.  One alone is known at compile time (52M bf16 to
+// MXFP4: 24.2 us for 25.7).
 template <bool MANY, typename Args>
 STRATA_DEVFN int job_of(const Jobs<Args>& j) {
   return MANY ? (blockIdx.x >= j.first[1]) + (blockIdx.x >= j.first[2]) : 0;
