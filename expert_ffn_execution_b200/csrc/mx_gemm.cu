@@ -1,19 +1,26 @@
 // mx_gemm.cu -- the many-token form of y = x w^T over microscaled matrices.
 //
 // With hundreds of tokens the product is bound by how fast operands reach the
-// tensor cores: an SM's share of the 4-bit rate is 61 TFLOP/s, and a tile of
-// m x n spends (m + n) / 2 bytes of L2 reads per k for 2 m n operations.  So
-// the tile is as large as tensor memory allows: a pair of CTAs (cta_group::2)
-// multiplies 256 tokens x 256 features, each CTA loading 128 rows of both and
-// holding 128 tokens x 256 features of the sums.
+// tensor cores: a tile of m x n reads (m + n) K elements from L2 for 2 m n K
+// operations, and the 148 SMs together get 11 to 13 TB/s.  So the tile is as
+// large as tensor memory allows: a pair of CTAs (cta_group::2) multiplies 256
+// tokens x 256 features, each CTA loading 128 rows of both and holding 128
+// tokens x 256 features of the sums.  T = 8192, N = 16384, K = 4096, 4x4 bits:
+// 431 us with 128 x 128 tiles of one CTA, 188 us (5.9 PFLOP/s) here; N =
+// 10240, K = 2560, 8x4 bits: 304 and 146 us (2.9 PFLOP/s); the tensor pipe is
+// active for 74 and 79 % of the cycles.  The order of the tiles makes no
+// difference (operands of this size stay in L2).
 //
-// Persistent, one pair a TPC-sized cluster: tiles in turn.  Per CTA: warps
-// 0-7 read the sums out (a lane quarter of 32 tokens, half of the features
-// each), warp 8 starts the copies, warp 9 of the even CTA issues the scale
-// copies and the MMAs of both.  The sums of a tile (256 columns) and the
-// stages' scales (12 columns per 128 of K) share the 512 columns, so the next
-// tile waits until the readers have the sums in registers; they are rounded,
-// turned in shared memory and stored while it runs.
+// Persistent: a pair takes tiles in turn.  Per CTA: warps 0-7 read the sums
+// out (a lane quarter of 32 tokens, half of the features each), warp 8 starts
+// the copies, warp 9 of the even CTA issues the scale copies and the MMAs of
+// both.  The sums of a tile (256 columns) and the stages' scales (12 columns
+// per 128 of K) share the 512 columns, so the next tile waits until the
+// readers have the sums in registers (500 cycles after the last MMA); they are
+// rounded, turned in shared memory and stored while it runs.  Halves of 128
+// features in three rotating buffers, which need not wait, are slower (229 us
+// when one buffer took 206): an MMA of 128 columns reads its other operand
+// twice as often.
 #include <algorithm>
 
 #include "deal.h"

@@ -5,7 +5,8 @@
 // and by the launch where it is small; in between, by instructions, so what is
 // not the conversion itself is kept small.  A thread takes 16 elements at a
 // time (half a block: one shuffle joins two lanes' largest magnitudes), and
-// loads its kQUnroll pieces, kQThreads apart, before it uses the first.
+// loads its kQUnroll pieces, kQThreads apart, before it uses the first (32
+// experts of 2560 x 640 to MXFP4: 83, 72 and 78 us with 1, 2 and 4).
 // Matrix, row and column of the first come from its flat index by division,
 // those of the next, and their offsets, by adding.  8192 x 4096 bf16 to FP8:
 // 36 us with 8 elements and three divisions a piece, 24 us without the
