@@ -125,6 +125,8 @@ class MXTensor(_Matrix):
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: int, rows: int, K: int,
                  layout: int):
+        if _fast and _fast.wrap(self, codes, scales, fmt, rows, K, layout):
+            return
         _check_format(fmt, rows, K, layout)
         for t, n, what in ((codes, _code_bytes(rows, fmt, K), "codes"),
                            (scales, _scale_bytes(rows, K, layout), "scales")):

@@ -294,6 +294,38 @@ PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {  // x, fmt,
   return reinterpret_cast<PyObject*>(m);
 }
 
+// q, codes, scales, fmt, rows, K, layout: fills in q; True where it did.
+PyObject* wrap(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Tensor codes, scales;
+  long fmt, rows, K, layout;
+  if (n != 7 || !is_mx(args[0]) || !read(args[1], &codes) || !read(args[2], &scales) ||
+      !small_int(args[3], &fmt) || !small_int(args[4], &rows) || !small_int(args[5], &K) ||
+      !small_int(args[6], &layout) || !format(fmt, rows, K, layout))
+    Py_RETURN_FALSE;
+  auto plane = [](const Tensor& t, int64_t bytes) {
+    if (t.dims == 1) return t.size[0] == bytes && (bytes <= 1 || t.stride[0] == 1);
+    return t.rows_contiguous() && t.size[0] * t.size[1] == bytes;
+  };
+  if (codes.dtype != 8 || scales.dtype != 8 || codes.index != scales.index ||
+      !plane(codes, code_bytes(rows, (int)fmt, K)) || !plane(scales, scale_bytes(rows, K, (int)layout)))
+    Py_RETURN_FALSE;
+  PyObject* dev = device_object(codes.index);
+  if (!dev) return nullptr;
+  Matrix* m = reinterpret_cast<Matrix*>(args[0]);
+  m->fmt = (int)fmt;
+  m->layout = (int)layout;
+  m->rows = rows;
+  m->K = K;
+  m->index = codes.index;
+  m->codes_ptr = codes.ptr;
+  m->scales_ptr = scales.ptr;
+  Py_XSETREF(m->device, Py_NewRef(dev));
+  Py_XSETREF(m->both, Py_NewRef(Py_None));
+  Py_XSETREF(m->codes, Py_NewRef(args[1]));
+  Py_XSETREF(m->scales, Py_NewRef(args[2]));
+  Py_RETURN_TRUE;
+}
+
 PyObject* dequantize(PyObject*, PyObject* const* args, Py_ssize_t n) {  // q, dtype, stream
   void* stream;
   if (n != 3 || !is_mx(args[0])) NOT_TAKEN;
@@ -463,6 +495,7 @@ PyObject* setup(PyObject*, PyObject* args) {
 
 PyMethodDef methods[] = {
     {"setup", setup, METH_VARARGS, "Hands over the library's functions and torch's."},
+    {"wrap", (PyCFunction)(void*)wrap, METH_FASTCALL, "MXTensor's fields; False where it does not take them."},
     {"quantize", (PyCFunction)(void*)quantize, METH_FASTCALL, "mx_quantize, or None."},
     {"dequantize", (PyCFunction)(void*)dequantize, METH_FASTCALL, "MXTensor.dequantize, or None."},
     {"add_rmsnorm", (PyCFunction)(void*)add_rmsnorm, METH_FASTCALL, "add_rmsnorm, or None."},

@@ -544,6 +544,17 @@ def test_native_calls_are_the_python_ones(monkeypatch):
             assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
 
 
+def test_native_tensors_are_the_python_ones(monkeypatch):
+    q = sm.mx_quantize(torch.randn(5, 160, device=DEV), sm.MX_FP4, sm.MX_ROWS)
+    made = []
+    for fast in (mx._fast, None):
+        monkeypatch.setattr(mx, "_fast", fast)
+        m = sm.MXTensor(q.codes, q.scales, sm.MX_FP4, 5, 160, sm.MX_ROWS)
+        made.append(tuple(getattr(m, f) for f in mx._FIELDS))
+        assert m.codes is q.codes and m.scales is q.scales
+    assert made[0] == made[1]
+
+
 def test_native_calls_keep_nothing():
     x = torch.randn(64, 256, device=DEV)
     d = torch.randn(64, 256, device=DEV)
@@ -557,6 +568,7 @@ def test_native_calls_keep_nothing():
     used = torch.cuda.memory_allocated()
     for _ in range(50):
         every_call(x, d, None, w, b)
+        sm.MXTensor(w.codes, w.scales, w.fmt, w.rows, w.K, w.layout)
     gc.collect()
     assert torch.cuda.memory_allocated() == used
     for before, o in zip(held, (x, d, w, b, torch.float32, x.device, sm.MXTensor)):
@@ -569,7 +581,15 @@ def test_native_calls_leave_refusals_to_python():
     q = sm.mx_quantize(x, sm.MX_FP8)
     rows = sm.mx_quantize(x, sm.MX_FP8, sm.MX_ROWS)
     w4 = sm.mx_quantize(x, sm.MX_FP4)
+    c, s = rows.codes, rows.scales
     for call, error, match in (
+            (lambda: sm.MXTensor(c, s, 3, 4, 128, sm.MX_ROWS), ValueError, "fmt"),
+            (lambda: sm.MXTensor(c, s, sm.MX_FP8, 4, 120, sm.MX_ROWS), ValueError, "multiple of 32"),
+            (lambda: sm.MXTensor(c, s, sm.MX_FP4, 4, 128, sm.MX_ROWS), ValueError, "codes"),
+            (lambda: sm.MXTensor(c, s[:3], sm.MX_FP8, 4, 128, sm.MX_ROWS), ValueError, "scales"),
+            (lambda: sm.MXTensor(c[:, ::2], s, sm.MX_FP4, 4, 128, sm.MX_ROWS), ValueError, "codes"),
+            (lambda: sm.MXTensor(c.int(), s, sm.MX_FP8, 4, 128, sm.MX_ROWS), ValueError, "codes"),
+            (lambda: sm.MXTensor(c, s.cpu(), sm.MX_FP8, 4, 128, sm.MX_ROWS), ValueError, "scales on"),
             (lambda: sm.mx_quantize(x.T, sm.MX_FP8), ValueError, "rows"),
             (lambda: sm.mx_quantize(x[:, 1:97], sm.MX_FP8), ValueError, "16-byte"),
             (lambda: sm.mx_quantize(x[:, :48], sm.MX_FP8), ValueError, "multiple of 32"),
