@@ -398,6 +398,44 @@ def test_linear_on_two_streams_at_once():
         assert torch.equal(y, want)
 
 
+# ---------------------------------------------------------------- past 32 bits
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows are those of a call with them alone."""
+    rows, K, tail = (1 << 19) + 5 + 128 * 37, 4096, 133
+    first = rows - rows % 128 - 128  # where a tile of scales starts
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device=DEV)
+    x[:1 << 17].normal_(generator=gen(90))
+    for at in range(1 << 17, rows, 1 << 17):
+        n = min(1 << 17, rows - at)
+        x[at:at + n] = x[:n]
+    x[first:].normal_(generator=gen(91))
+    for fmt in FMTS:
+        q = sm.mx_quantize(x, fmt)
+        alone = sm.mx_quantize(x[first:], fmt)
+        assert torch.equal(q.codes[first:], alone.codes)
+        assert torch.equal(q.scales[first * K // 32:], alone.scales)
+        v = q.dequantize(torch.bfloat16)
+        assert torch.equal(v[-tail:], alone.dequantize(torch.bfloat16)[-tail:])
+        assert torch.equal(v[:300], sm.mx_quantize(x[:300], fmt).dequantize(torch.bfloat16))
+        del v, q
+    n = sm.add_rmsnorm(x, fmt=sm.MX_FP8, residual_out=x)
+    alone = sm.add_rmsnorm(x[first:].clone(), fmt=sm.MX_FP8)
+    assert torch.equal(n.mx.codes[first:], alone.mx.codes)
+    assert torch.equal(n.mx.scales[first * K // 32:], alone.mx.scales)
+    del x, n, alone
+    torch.cuda.empty_cache()
+    T, N, K = (1 << 17) + 77, 17000, 128
+    a, w = sm.mx_quantize(torch.randn(T, K, device=DEV), sm.MX_FP8), sm.mx_quantize(torch.randn(N, K, device=DEV), sm.MX_FP4)
+    last = T - T % 128 - 256
+    z = sm.MXTensor(a.codes[last:], a.scales[last * K // 32:].clone(), sm.MX_FP8, T - last, K, sm.MX_TILES)
+    for dtype in (torch.bfloat16, torch.float32):
+        y = sm.mx_linear(a, w, out_dtype=dtype)
+        assert y.numel() > 1 << 31
+        assert torch.equal(y[last:], sm.mx_linear(z, w, out_dtype=dtype))
+        del y
+        torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- together
 def step(x, d, gain, w, out):
     n = sm.add_rmsnorm(x, d, gain, fmt=sm.MX_FP8, residual_out=x)
