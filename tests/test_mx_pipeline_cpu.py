@@ -230,7 +230,7 @@ def test_the_model_is_of_the_kernels():
         assert line in gemm, line
     linear = open(os.path.join(CSRC, "mx_linear.cu")).read()
     for line in ("mbar_init(&full[threadIdx.x], 1);", "uint32_t ph = 1;", "uint32_t ph = 0;", "if (++s == S) s = 0, ph ^= 1u;",
-                 "per = (nt + splits - 1) / splits;", "mine = max(0, min(per, nt - first));",
+                 "per = (nt + splits - 1) >> lg_splits;", "mine = max(0, min(per, nt - first));",
                  "(uint32_t)(mine * splits * C::token)", "count = min(per, nt - to * per);"):
         assert line in linear, line
-    assert re.search(r"chunks \* \(rank \+ 1\) / splits\) - c0", linear)
+    assert re.search(r"chunks \* \(rank \+ 1\) >> lg_splits\) - c0", linear)
