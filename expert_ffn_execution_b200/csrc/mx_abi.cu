@@ -91,8 +91,9 @@ int32_t moe_mx_dequantize(const void* codes, uint64_t codes_batch_stride, const 
                                 scales_batch_stride);
   if (r != STRATA_OK) return r;
   if ((rows > 1 && dst_row_stride < K) ||
-      (batch > 1 && dst_batch_stride < (rows - 1) * dst_row_stride + K &&
-       dst_row_stride < (batch - 1) * dst_batch_stride + K))
+      (batch > 1 && (dst_batch_stride < K ||
+                     (dst_batch_stride < (rows - 1) * dst_row_stride + K &&
+                      dst_row_stride < (batch - 1) * dst_batch_stride + K))))
     return STRATA_EINVAL;  // rows of dst would overlap
   if (batch == 0 || rows == 0) return STRATA_OK;
   MxDequantArgs a = {};
@@ -178,6 +179,7 @@ int32_t moe_mx_unpack_experts(const void* blobs, uint64_t blob_stride, int32_t E
 
 int32_t moe_mx_tile_scales(const void* scales, int32_t rows, int32_t K, void* tiles, void* stream) {
   if (rows < 0 || K < kMxBlock || K % kMxBlock) return STRATA_EINVAL;
+  if (mx_scale_plane(rows, K, STRATA_MX_TILES) >= (int64_t)1 << 40) return STRATA_EINVAL;
   if (rows == 0) return STRATA_OK;
   if (!scales || !tiles || !aligned(tiles, 16)) return STRATA_EINVAL;
   return from_cuda(launch_mx_tile_scales(reinterpret_cast<const uint8_t*>(scales), rows, K,

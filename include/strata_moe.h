@@ -449,8 +449,8 @@ STRATA_API int32_t moe_mx_unpack_experts(const void* blobs, uint64_t blob_stride
 
 /* Scales from STRATA_MX_ROWS to STRATA_MX_TILES (both of one [rows, K]
  * matrix): what a checkpoint's scales need once before moe_mx_linear reads
- * them.  tiles 16-byte aligned, moe_mx_scale_bytes() bytes; rows == 0 is a
- * no-op. */
+ * them.  tiles 16-byte aligned, moe_mx_scale_bytes() bytes, below 2^40;
+ * rows == 0 is a no-op. */
 STRATA_API int32_t moe_mx_tile_scales(const void* scales, int32_t rows, int32_t K, void* tiles,
                            void* stream);
 

@@ -87,6 +87,18 @@ def test_dequantize_refuses(k):
     assert dequant(**k) == B.EINVAL
 
 
+@pytest.mark.parametrize("k", [
+    dict(batch=2, dst_row_stride=512, dst_batch_stride=0), dict(batch=2, rows=1, dst_batch_stride=0),
+    dict(batch=2, rows=1, dst_batch_stride=56), dict(batch=3, dst_row_stride=128, dst_batch_stride=64)],
+    ids=str)
+def test_dequantize_refuses_matrices_that_overlap(k):
+    assert dequant(**k) == B.EINVAL
+
+
+def test_tile_scales_refuses_planes_past_memory():
+    assert sm.moe_mx_tile_scales(P, (1 << 31) - 1, 1 << 30, P, stream=0, check=False) == B.EINVAL
+
+
 def test_tile_scales_refuses():
     for a in ((P, -1, 64, P), (P, 4, 48, P), (None, 4, 64, P), (P, 4, 64, None), (P, 4, 64, P + 8)):
         assert sm.moe_mx_tile_scales(*a, stream=0, check=False) == B.EINVAL
