@@ -2,7 +2,7 @@
 
 Each .cu under csrc/ is compiled to an object (in parallel) and linked into one
 shared library next to this file; native/mxcalls.cpp becomes the Python module
-_mxcalls beside it (g++, the CPython headers).  Run `python -m expert_ffn_execution_b200.build`.
+_mxcalls beside it (g++, the CPython and torch headers).  Run `python -m expert_ffn_execution_b200.build`.
 """
 from __future__ import annotations
 
@@ -62,9 +62,16 @@ def build_calls(force: bool = False) -> str:
     if not force and os.path.exists(CALLS) and all(
             os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
         return CALLS
+    import torch  # its headers and libraries, which are loaded before the module is
+    at = os.path.join(os.path.dirname(torch.__file__), "include")
+    libs = ("c10", "c10_cuda", "torch_cpu", "torch_cuda", "torch_python")
+    cuda = os.path.dirname(os.path.dirname(NVCC))
     cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-Wall", "-shared", "-fPIC",
-           "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, CALLS_SRC,
-           "-o", CALLS + ".tmp"]
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DSTRATA_TORCH="{torch.__version__}"', "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           "-isystem", at, "-isystem", os.path.join(at, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), CALLS_SRC, "-o", CALLS + ".tmp",
+           "-L", os.path.join(os.path.dirname(at), "lib"), *("-l" + n for n in libs)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stderr}")

@@ -9,13 +9,25 @@
 // raise, changes the device.  So every rule and every message is mx.py's, and
 // without this module everything works, later.
 //
-// Only the CPython interface is used: tensors are read through their Python
-// attributes and made by torch.empty.
+// Tensors are read and made through ATen: reading one through its Python
+// attributes took 0.35 us, making one by a Python call of torch.empty 1.6 us.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stddef.h>
 #include <stdint.h>
 #include <structmember.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Device.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <exception>
+#include <new>
 
 #include "strata_moe.h"
 
@@ -28,23 +40,13 @@ struct Library {
   decltype(&moe_add_rmsnorm) add_rmsnorm;
   decltype(&moe_mx_linear) linear;
 } lib;
-PyObject* torch_empty;     // torch.empty
 PyObject* torch_tensor;    // torch.Tensor
 PyObject* torch_param;     // torch.nn.Parameter
-PyObject* current_device;  // () -> index
-PyObject* current_stream;  // index -> handle
-PyObject* dtypes[3];       // float32, float16, bfloat16, by STRATA_DTYPE_*
-PyObject* uint8;
-PyObject* int32;
 PyTypeObject* matrix_type; // Matrix below
 PyTypeObject* mx_type;     // mx.py's MXTensor, a subclass of it
-PyObject* add_norm;        // mx.py's AddNorm
+PyTypeObject* norm_type;   // mx.py's AddNorm, a named tuple
 PyObject* devices[64];     // torch.device("cuda", i), as they are met
-PyObject* torch_device;
-
-// interned names
-PyObject *s_shape, *s_stride, *s_dtype, *s_data_ptr, *s_get_device, *s_cuda_stream, *s_cuda;
-PyObject *kw_empty;  // ("dtype", "device")
+PyObject* s_cuda_stream;   // an interned name
 
 // ---------------------------------------------------------------- MXTensor's fields
 struct Matrix {
@@ -54,14 +56,20 @@ struct Matrix {
   unsigned long long codes_ptr, scales_ptr;
   int index;  // of the CUDA device, -1: none
   PyObject* device;
-  PyObject *both, *codes, *scales;  // one allocation, or the two planes' tensors
+  at::Tensor both;           // one allocation for both planes, or
+  PyObject *codes, *scales;  // the two planes' tensors
 };
+
+PyObject* matrix_new(PyTypeObject* type, PyObject*, PyObject*) {
+  PyObject* o = type->tp_alloc(type, 0);
+  if (o) new (&reinterpret_cast<Matrix*>(o)->both) at::Tensor();
+  return o;
+}
 
 int matrix_traverse(PyObject* o, visitproc visit, void* arg) {
   Matrix* m = reinterpret_cast<Matrix*>(o);
   Py_VISIT(Py_TYPE(o));
   Py_VISIT(m->device);
-  Py_VISIT(m->both);
   Py_VISIT(m->codes);
   Py_VISIT(m->scales);
   return 0;
@@ -69,7 +77,6 @@ int matrix_traverse(PyObject* o, visitproc visit, void* arg) {
 int matrix_clear(PyObject* o) {
   Matrix* m = reinterpret_cast<Matrix*>(o);
   Py_CLEAR(m->device);
-  Py_CLEAR(m->both);
   Py_CLEAR(m->codes);
   Py_CLEAR(m->scales);
   return 0;
@@ -78,6 +85,7 @@ void matrix_dealloc(PyObject* o) {
   PyTypeObject* type = Py_TYPE(o);
   PyObject_GC_UnTrack(o);
   matrix_clear(o);
+  reinterpret_cast<Matrix*>(o)->both.~Tensor();
   type->tp_free(o);
   Py_DECREF(type);
 }
@@ -90,11 +98,27 @@ PyMemberDef matrix_members[] = {
     {"scales_ptr", T_ULONGLONG, offsetof(Matrix, scales_ptr), 0, nullptr},
     {"index", T_INT, offsetof(Matrix, index), 0, nullptr},
     {"device", T_OBJECT, offsetof(Matrix, device), 0, nullptr},
-    {"_both", T_OBJECT, offsetof(Matrix, both), 0, nullptr},
     {"_codes", T_OBJECT, offsetof(Matrix, codes), 0, nullptr},
     {"_scales", T_OBJECT, offsetof(Matrix, scales), 0, nullptr},
     {nullptr, 0, 0, 0, nullptr}};
-PyType_Slot matrix_slots[] = {{Py_tp_traverse, (void*)matrix_traverse},
+PyObject* get_both(PyObject* o, void*) {
+  const at::Tensor& t = reinterpret_cast<Matrix*>(o)->both;
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(t);
+}
+int set_both(PyObject* o, PyObject* v, void*) {
+  if (v && v != Py_None && !THPVariable_Check(v)) {
+    PyErr_SetString(PyExc_TypeError, "a tensor or None is wanted");
+    return -1;
+  }
+  reinterpret_cast<Matrix*>(o)->both = v && v != Py_None ? THPVariable_Unpack(v) : at::Tensor();
+  return 0;
+}
+PyGetSetDef matrix_getset[] = {{"_both", get_both, set_both, nullptr, nullptr},
+                               {nullptr, nullptr, nullptr, nullptr, nullptr}};
+PyType_Slot matrix_slots[] = {{Py_tp_new, (void*)matrix_new},
+                              {Py_tp_getset, (void*)matrix_getset},
+                              {Py_tp_traverse, (void*)matrix_traverse},
                               {Py_tp_clear, (void*)matrix_clear},
                               {Py_tp_dealloc, (void*)matrix_dealloc},
                               {Py_tp_members, (void*)matrix_members},
@@ -112,10 +136,20 @@ bool pass() {
   return false;
 }
 
+int dtype_of(at::ScalarType t) {
+  return t == at::kFloat ? STRATA_DTYPE_F32 : t == at::kHalf ? STRATA_DTYPE_F16 : t == at::kBFloat16 ? STRATA_DTYPE_BF16 : -1;
+}
+int dtype_of(PyObject* o) {
+  return THPDtype_Check(o) ? dtype_of(reinterpret_cast<THPDtype*>(o)->scalar_type) : -1;
+}
+at::ScalarType scalar_type(int dt) {
+  return dt == STRATA_DTYPE_F32 ? at::kFloat : dt == STRATA_DTYPE_F16 ? at::kHalf : at::kBFloat16;
+}
+
 struct Tensor {
   int dtype = -1;  // STRATA_DTYPE_*, 8: uint8, 32: int32
   int index = -1;
-  uint64_t ptr = 0;
+  void* ptr = nullptr;
   int dims = 0;
   int64_t size[2] = {0, 0}, stride[2] = {0, 0};
   bool rows_contiguous() const {
@@ -124,91 +158,55 @@ struct Tensor {
   }
 };
 
-bool number(PyObject* o, int64_t* v) {  // steals o
-  if (!o) return pass();
-  *v = PyLong_AsLongLong(o);
-  Py_DECREF(o);
-  return !(*v == -1 && PyErr_Occurred()) || pass();
-}
-
-// Reads a torch.Tensor (or Parameter; no other subclass) of one or two dimensions.
+// Reads a torch.Tensor (or Parameter; no other subclass) of one or two
+// dimensions on a CUDA device.  Throws for one without memory of its own.
 bool read(PyObject* o, Tensor* t) {
   PyObject* type = reinterpret_cast<PyObject*>(Py_TYPE(o));
   if (type != torch_tensor && type != torch_param) return false;
-  PyObject* d = PyObject_GetAttr(o, s_dtype);
-  if (!d) return pass();
-  t->dtype = d == dtypes[0] ? 0 : d == dtypes[1] ? 1 : d == dtypes[2] ? 2 : d == uint8 ? 8 : d == int32 ? 32 : -1;
-  Py_DECREF(d);
-  if (t->dtype < 0) return false;
-  int64_t v;
-  if (!number(PyObject_CallMethodNoArgs(o, s_get_device), &v) || v < 0 || v >= 64) return false;
-  t->index = (int)v;
-  if (!number(PyObject_CallMethodNoArgs(o, s_data_ptr), &v)) return false;
-  t->ptr = (uint64_t)v;
-  PyObject* shape = PyObject_GetAttr(o, s_shape);
-  PyObject* stride = PyObject_CallMethodNoArgs(o, s_stride);
-  bool ok = shape && stride && PyTuple_Check(shape) && PyTuple_Check(stride);
-  if (ok) {
-    t->dims = (int)PyTuple_GET_SIZE(shape);
-    ok = (t->dims == 1 || t->dims == 2) && PyTuple_GET_SIZE(stride) == t->dims;
-    for (int i = 0; ok && i < t->dims; ++i) {
-      t->size[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i));
-      t->stride[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, i));
-    }
+  const at::Tensor& v = THPVariable_Unpack(o);
+  if (!v.is_cuda() || v.layout() != at::kStrided || v.is_neg()) return false;
+  const at::ScalarType st = v.scalar_type();
+  t->dtype = st == at::kByte ? 8 : st == at::kInt ? 32 : dtype_of(st);
+  t->index = v.device().index();
+  t->dims = (int)v.dim();
+  if (t->dtype < 0 || t->index < 0 || t->index >= 64 || (t->dims != 1 && t->dims != 2)) return false;
+  const at::IntArrayRef size = v.sizes(), stride = v.strides();
+  for (int i = 0; i < t->dims; ++i) {
+    t->size[i] = size[i];
+    t->stride[i] = stride[i];
   }
-  Py_XDECREF(shape);
-  Py_XDECREF(stride);
-  return PyErr_Occurred() || !ok ? pass() : true;
+  t->ptr = v.data_ptr();
+  return true;
 }
 
 bool is_mx(PyObject* o) { return Py_TYPE(o) == mx_type; }
 
-int dtype_of(PyObject* o) { return o == dtypes[0] ? 0 : o == dtypes[1] ? 1 : o == dtypes[2] ? 2 : -1; }
-
 // The stream's handle on device `index`, which has to be the current one.
 bool target(int index, PyObject* stream, void** handle) {
-  int64_t v;
-  if (!number(PyObject_CallNoArgs(current_device), &v) || v != index) return false;
-  PyObject* s;
+  if (c10::impl::TorchDispatchModeTLS::any_modes_set() || c10::cuda::current_device() != index)
+    return false;
   if (stream == Py_None) {
-    PyObject* i = PyLong_FromLong(index);
-    if (!i) return pass();
-    s = PyObject_CallOneArg(current_stream, i);
-    Py_DECREF(i);
-  } else if (PyLong_Check(stream)) {
-    s = Py_NewRef(stream);
-  } else {
-    s = PyObject_GetAttr(stream, s_cuda_stream);
+    *handle = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
+    return true;
   }
-  if (!number(s, &v)) return false;
+  PyObject* s = PyLong_Check(stream) ? Py_NewRef(stream) : PyObject_GetAttr(stream, s_cuda_stream);
+  if (!s) return pass();
+  const long long v = PyLong_AsLongLong(s);
+  Py_DECREF(s);
+  if (v == -1 && PyErr_Occurred()) return pass();
   *handle = reinterpret_cast<void*>(v);
   return true;
 }
 
 PyObject* device_object(int index) {  // borrowed
   if (!devices[index])
-    devices[index] = PyObject_CallFunction(torch_device, "Oi", s_cuda, index);
+    devices[index] = THPDevice_New(at::Device(at::kCUDA, (c10::DeviceIndex)index));
   return devices[index];
 }
 
-// torch.empty(a[, b], dtype=dtype, device=device): a new reference, and its address.
-PyObject* empty(int dims, int64_t a, int64_t b, PyObject* dtype, PyObject* device, uint64_t* ptr) {
-  PyObject* args[5] = {nullptr, PyLong_FromLongLong(a), nullptr, nullptr, nullptr};
-  int n = 1;
-  if (dims == 2) args[1 + n++] = PyLong_FromLongLong(b);
-  args[1 + n] = dtype;
-  args[2 + n] = device;
-  PyObject* t = nullptr;
-  if (args[1] && args[n])
-    t = PyObject_Vectorcall(torch_empty, args + 1, (size_t)n | PY_VECTORCALL_ARGUMENTS_OFFSET, kw_empty);
-  Py_XDECREF(args[1]);
-  if (dims == 2) Py_XDECREF(args[2]);
-  if (!t) return nullptr;
-  PyObject* p = PyObject_CallMethodNoArgs(t, s_data_ptr);
-  *ptr = p ? PyLong_AsUnsignedLongLong(p) : 0;
-  Py_XDECREF(p);
-  if (PyErr_Occurred()) Py_CLEAR(t);
-  return t;
+at::Tensor empty(at::IntArrayRef size, at::ScalarType type, int index) {
+  return at::Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, (c10::DeviceIndex)index),
+                                           std::nullopt));
 }
 
 int64_t code_bytes(int64_t rows, int fmt, int64_t K) { return rows * (fmt == STRATA_MX_FP4 ? K / 2 : K); }
@@ -221,39 +219,58 @@ bool format(long fmt, int64_t rows, int64_t K, long layout) {
          K >= 32 && K < 1LL << 31 && K % 32 == 0;
 }
 
-// An MXTensor to be written by a call, both planes in one allocation.
-Matrix* new_matrix(int fmt, int64_t rows, int64_t K, int layout, int index) {
-  PyObject* dev = device_object(index);
-  if (!dev) return nullptr;
-  Matrix* m = reinterpret_cast<Matrix*>(mx_type->tp_alloc(mx_type, 0));
-  if (!m) return nullptr;
-  const int64_t at = (code_bytes(rows, fmt, K) + 255) & ~(int64_t)255;
-  uint64_t ptr = 0;
-  m->both = empty(1, at + scale_bytes(rows, K, layout), 0, uint8, dev, &ptr);
-  if (!m->both) {
-    Py_DECREF(m);
-    return nullptr;
+// Memory for an MXTensor that a call writes, both planes in one allocation.
+struct Planes {
+  at::Tensor both;
+  uint8_t *codes = nullptr, *scales = nullptr;
+  Planes() = default;
+  Planes(int fmt, int64_t rows, int64_t K, int layout, int index) {
+    const int64_t at = (code_bytes(rows, fmt, K) + 255) & ~(int64_t)255;
+    both = empty({at + scale_bytes(rows, K, layout)}, at::kByte, index);
+    codes = static_cast<uint8_t*>(both.data_ptr());
+    scales = codes + at;
   }
+};
+PyObject* new_matrix(Planes&& p, int fmt, int64_t rows, int64_t K, int layout, int index) {
+  PyObject* dev = device_object(index);
+  PyObject* o = dev ? matrix_new(mx_type, nullptr, nullptr) : nullptr;
+  if (!o) return nullptr;
+  Matrix* m = reinterpret_cast<Matrix*>(o);
   m->fmt = fmt;
   m->layout = layout;
   m->rows = rows;
   m->K = K;
   m->index = index;
   m->device = Py_NewRef(dev);
-  m->codes = Py_NewRef(Py_None);
-  m->scales = Py_NewRef(Py_None);
-  m->codes_ptr = ptr;
-  m->scales_ptr = ptr + at;
-  return m;
+  m->codes_ptr = reinterpret_cast<uintptr_t>(p.codes);
+  m->scales_ptr = reinterpret_cast<uintptr_t>(p.scales);
+  m->both = std::move(p.both);
+  return o;
 }
 
+// Makes the outputs and calls the library without the interpreter's lock (a
+// call may wait for the allocator or the device).  Anything but STRATA_OK, an
+// exception among it, leaves the call to mx.py.
 template <typename F>
 int32_t launch(F f) {
-  int32_t rc;
+  int32_t rc = STRATA_ECUDA;
   Py_BEGIN_ALLOW_THREADS
-  rc = f();
+  try {
+    rc = f();
+  } catch (const std::exception&) {
+  }
   Py_END_ALLOW_THREADS
   return rc;
+}
+// A call's own part: exceptions (a tensor without memory of its own) are None.
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  try {
+    return F(args, n);
+  } catch (const std::exception&) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
 }
 
 bool small_int(PyObject* o, long* v) {
@@ -271,7 +288,7 @@ bool small_int(PyObject* o, long* v) {
 // Each returns None for a call it does not take, and for one that the library
 // refuses (nothing was enqueued then; mx.py's own call says why).
 
-PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {  // x, fmt, layout, stream
+PyObject* quantize(PyObject* const* args, Py_ssize_t n) {  // x, fmt, layout, stream
   Tensor x;
   long fmt, layout;
   void* stream;
@@ -280,35 +297,31 @@ PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {  // x, fmt,
       !target(x.index, args[3], &stream))
     NOT_TAKEN;
   if (x.size[0] > 0 && x.stride[1] != 1) NOT_TAKEN;
-  Matrix* m = new_matrix((int)fmt, x.size[0], x.size[1], (int)layout, x.index);
-  if (!m) return nullptr;
+  Planes p;
   const int32_t rc = launch([&] {
-    return lib.quantize(reinterpret_cast<const void*>(x.ptr), x.dtype, 1, (int32_t)m->rows,
-                        (int32_t)m->K, x.stride[0], 0, m->fmt, reinterpret_cast<void*>(m->codes_ptr), 0,
-                        reinterpret_cast<void*>(m->scales_ptr), m->layout, 0, stream);
+    p = Planes((int)fmt, x.size[0], x.size[1], (int)layout, x.index);
+    return lib.quantize(x.ptr, x.dtype, 1, (int32_t)x.size[0], (int32_t)x.size[1], x.stride[0], 0,
+                        (int32_t)fmt, p.codes, 0, p.scales, (int32_t)layout, 0, stream);
   });
-  if (rc != STRATA_OK) {
-    Py_DECREF(m);
-    NOT_TAKEN;
-  }
-  return reinterpret_cast<PyObject*>(m);
+  if (rc != STRATA_OK) NOT_TAKEN;
+  return new_matrix(std::move(p), (int)fmt, x.size[0], x.size[1], (int)layout, x.index);
 }
 
 // q, codes, scales, fmt, rows, K, layout: fills in q; True where it did.
-PyObject* wrap(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* wrap(PyObject* const* args, Py_ssize_t n) {
   Tensor codes, scales;
   long fmt, rows, K, layout;
-  if (n != 7 || !is_mx(args[0]) || !read(args[1], &codes) || !read(args[2], &scales) ||
-      !small_int(args[3], &fmt) || !small_int(args[4], &rows) || !small_int(args[5], &K) ||
-      !small_int(args[6], &layout) || !format(fmt, rows, K, layout))
-    Py_RETURN_FALSE;
+  if (n != 7 || !is_mx(args[0]) || !small_int(args[3], &fmt) || !small_int(args[4], &rows) ||
+      !small_int(args[5], &K) || !small_int(args[6], &layout) || !format(fmt, rows, K, layout) ||
+      !read(args[1], &codes) || !read(args[2], &scales))
+    NOT_TAKEN;
   auto plane = [](const Tensor& t, int64_t bytes) {
     if (t.dims == 1) return t.size[0] == bytes && (bytes <= 1 || t.stride[0] == 1);
     return t.rows_contiguous() && t.size[0] * t.size[1] == bytes;
   };
   if (codes.dtype != 8 || scales.dtype != 8 || codes.index != scales.index ||
       !plane(codes, code_bytes(rows, (int)fmt, K)) || !plane(scales, scale_bytes(rows, K, (int)layout)))
-    Py_RETURN_FALSE;
+    NOT_TAKEN;
   PyObject* dev = device_object(codes.index);
   if (!dev) return nullptr;
   Matrix* m = reinterpret_cast<Matrix*>(args[0]);
@@ -317,39 +330,35 @@ PyObject* wrap(PyObject*, PyObject* const* args, Py_ssize_t n) {
   m->rows = rows;
   m->K = K;
   m->index = codes.index;
-  m->codes_ptr = codes.ptr;
-  m->scales_ptr = scales.ptr;
+  m->codes_ptr = reinterpret_cast<uintptr_t>(codes.ptr);
+  m->scales_ptr = reinterpret_cast<uintptr_t>(scales.ptr);
+  m->both = at::Tensor();
   Py_XSETREF(m->device, Py_NewRef(dev));
-  Py_XSETREF(m->both, Py_NewRef(Py_None));
   Py_XSETREF(m->codes, Py_NewRef(args[1]));
   Py_XSETREF(m->scales, Py_NewRef(args[2]));
   Py_RETURN_TRUE;
 }
 
-PyObject* dequantize(PyObject*, PyObject* const* args, Py_ssize_t n) {  // q, dtype, stream
+PyObject* dequantize(PyObject* const* args, Py_ssize_t n) {  // q, dtype, stream
   void* stream;
   if (n != 3 || !is_mx(args[0])) NOT_TAKEN;
-  Matrix* m = reinterpret_cast<Matrix*>(args[0]);
+  const Matrix& m = *reinterpret_cast<Matrix*>(args[0]);
   const int dt = dtype_of(args[1]);
-  if (dt < 0 || m->index < 0 || !target(m->index, args[2], &stream)) NOT_TAKEN;
-  uint64_t ptr = 0;
-  PyObject* out = empty(2, m->rows, m->K, args[1], m->device, &ptr);
-  if (!out) return nullptr;
-  const int32_t rc = launch([&] {
-    return lib.dequantize(reinterpret_cast<const void*>(m->codes_ptr), 0,
-                          reinterpret_cast<const void*>(m->scales_ptr), m->layout, 0, m->fmt, 1,
-                          (int32_t)m->rows, (int32_t)m->K, reinterpret_cast<void*>(ptr), dt, m->K, 0,
-                          stream);
-  });
-  if (rc != STRATA_OK) {
-    Py_DECREF(out);
+  if (dt < 0 || !m.device || m.device == Py_None || m.index < 0 || !target(m.index, args[2], &stream))
     NOT_TAKEN;
-  }
-  return out;
+  at::Tensor out;
+  const int32_t rc = launch([&] {
+    out = empty({(int64_t)m.rows, (int64_t)m.K}, scalar_type(dt), m.index);
+    return lib.dequantize(reinterpret_cast<const void*>(m.codes_ptr), 0,
+                          reinterpret_cast<const void*>(m.scales_ptr), m.layout, 0, m.fmt, 1,
+                          (int32_t)m.rows, (int32_t)m.K, out.data_ptr(), dt, m.K, 0, stream);
+  });
+  if (rc != STRATA_OK) NOT_TAKEN;
+  return THPVariable_Wrap(std::move(out));
 }
 
 // x, delta, gain, eps, out_dtype, fmt, layout, residual_out, stream
-PyObject* add_rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* add_rmsnorm(PyObject* const* args, Py_ssize_t n) {
   Tensor x, delta, gain, res;
   long fmt, layout;
   void* stream;
@@ -372,134 +381,115 @@ PyObject* add_rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
                    (gain.size[0] > 1 && gain.stride[0] != 1)))
     NOT_TAKEN;
   if (!target(x.index, args[8], &stream)) NOT_TAKEN;
-  PyObject* dev = device_object(x.index);
-  if (!dev) return nullptr;
-  PyObject *r = nullptr, *out = nullptr, *result = nullptr;
-  Matrix* m = nullptr;
-  uint64_t r_ptr = 0, out_ptr = 0;
-  int32_t rc = STRATA_OK;
-  if (has_res) {
-    r = Py_NewRef(args[7]);
-    r_ptr = res.ptr;
-  } else if (has_delta) {
-    r = empty(2, x.size[0], x.size[1], dtypes[x.dtype], dev, &r_ptr);
-    if (!r) goto end;
-  } else {
-    r = Py_NewRef(args[0]);
-  }
-  if (has_out) {
-    out = empty(2, x.size[0], x.size[1], args[4], dev, &out_ptr);
-    if (!out) goto end;
-  } else {
-    out = Py_NewRef(Py_None);
-  }
-  if (fmt && !(m = new_matrix((int)fmt, x.size[0], x.size[1], (int)layout, x.index))) goto end;
-  rc = launch([&] {
-    return lib.add_rmsnorm(
-        reinterpret_cast<const void*>(x.ptr), x.dtype, reinterpret_cast<const void*>(delta.ptr),
-        has_delta ? delta.dtype : 0, reinterpret_cast<const float*>(gain.ptr), (int32_t)x.size[0],
-        (int32_t)x.size[1], (float)PyFloat_AS_DOUBLE(args[3]), reinterpret_cast<void*>(r_ptr),
-        reinterpret_cast<void*>(out_ptr), od, (int32_t)fmt,
-        reinterpret_cast<void*>(m ? m->codes_ptr : 0), reinterpret_cast<void*>(m ? m->scales_ptr : 0),
-        (int32_t)layout, stream);
+  const float eps = (float)PyFloat_AS_DOUBLE(args[3]);
+  at::Tensor r, out;
+  Planes p;
+  const int32_t rc = launch([&] {
+    if (has_delta && !has_res) {
+      r = empty({x.size[0], x.size[1]}, scalar_type(x.dtype), x.index);
+      res.ptr = r.data_ptr();
+    }
+    if (has_out) out = empty({x.size[0], x.size[1]}, scalar_type(od), x.index);
+    if (fmt) p = Planes((int)fmt, x.size[0], x.size[1], (int)layout, x.index);
+    return lib.add_rmsnorm(x.ptr, x.dtype, delta.ptr, has_delta ? delta.dtype : 0,
+                           static_cast<const float*>(gain.ptr), (int32_t)x.size[0],
+                           (int32_t)x.size[1], eps, res.ptr, has_out ? out.data_ptr() : nullptr, od,
+                           (int32_t)fmt, p.codes, p.scales, (int32_t)layout, stream);
   });
-  if (rc == STRATA_OK) {
-    PyObject* parts[3] = {r, out, m ? reinterpret_cast<PyObject*>(m) : Py_None};
-    result = PyObject_Vectorcall(add_norm, parts, 3, nullptr);
-  } else {
-    result = Py_NewRef(Py_None);
+  if (rc != STRATA_OK) NOT_TAKEN;
+  // AddNorm((residual, out, mx)), by the tuple's constructor
+  PyObject* parts = PyTuple_New(3);
+  PyObject* one = parts ? PyTuple_Pack(1, parts) : nullptr;
+  PyObject* result = nullptr;
+  if (one) {
+    PyObject* a = has_res ? Py_NewRef(args[7]) : has_delta ? THPVariable_Wrap(std::move(r)) : Py_NewRef(args[0]);
+    PyObject* b = has_out ? THPVariable_Wrap(std::move(out)) : Py_NewRef(Py_None);
+    PyObject* c = fmt ? new_matrix(std::move(p), (int)fmt, x.size[0], x.size[1], (int)layout, x.index)
+                      : Py_NewRef(Py_None);
+    PyTuple_SET_ITEM(parts, 0, a);
+    PyTuple_SET_ITEM(parts, 1, b);
+    PyTuple_SET_ITEM(parts, 2, c);
+    if (a && b && c) result = PyTuple_Type.tp_new(norm_type, one, nullptr);
   }
-end:
-  Py_XDECREF(r);
-  Py_XDECREF(out);
-  Py_XDECREF(m);
+  Py_XDECREF(one);
+  Py_XDECREF(parts);
   return result;
 }
 
 // x, w, bias, out_dtype, out, dev_status, stream
-PyObject* linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
+PyObject* linear(PyObject* const* args, Py_ssize_t n) {
   if (n != 7 || !is_mx(args[0]) || !is_mx(args[1])) NOT_TAKEN;
-  Matrix *x = reinterpret_cast<Matrix*>(args[0]), *w = reinterpret_cast<Matrix*>(args[1]);
+  const Matrix &x = *reinterpret_cast<Matrix*>(args[0]), &w = *reinterpret_cast<Matrix*>(args[1]);
   Tensor bias, out, status;
   void* stream;
-  if (x->K != w->K || x->layout != STRATA_MX_TILES || w->layout != STRATA_MX_TILES || x->index < 0 ||
-      x->index != w->index)
+  if (x.K != w.K || x.layout != STRATA_MX_TILES || w.layout != STRATA_MX_TILES || x.index < 0 ||
+      x.index != w.index)
     NOT_TAKEN;
   const bool has_bias = args[2] != Py_None, has_out = args[4] != Py_None;
-  if (has_bias && (!read(args[2], &bias) || bias.dtype != 0 || bias.index != x->index ||
-                   bias.dims != 1 || bias.size[0] != w->rows || (bias.size[0] > 1 && bias.stride[0] != 1)))
+  if (has_bias && (!read(args[2], &bias) || bias.dtype != 0 || bias.index != x.index ||
+                   bias.dims != 1 || bias.size[0] != w.rows || (bias.size[0] > 1 && bias.stride[0] != 1)))
     NOT_TAKEN;
   if (args[5] != Py_None && (!read(args[5], &status) || status.dtype != 32 ||
-                             status.index != x->index || status.dims != 1 || status.size[0] < 1))
+                             status.index != x.index || status.dims != 1 || status.size[0] < 1))
     NOT_TAKEN;
-  int64_t ldy = w->rows;
+  int64_t ldy = w.rows;
   int dt = has_out ? -1 : dtype_of(args[3]);
   if (has_out) {
-    if (!read(args[4], &out) || out.dtype > 2 || out.index != x->index || out.dims != 2 ||
-        out.size[0] != x->rows || out.size[1] != w->rows || (w->rows > 1 && out.stride[1] != 1) ||
-        (x->rows > 1 && out.stride[0] < w->rows))
+    if (!read(args[4], &out) || out.dtype > 2 || out.index != x.index || out.dims != 2 ||
+        out.size[0] != x.rows || out.size[1] != w.rows || (w.rows > 1 && out.stride[1] != 1) ||
+        (x.rows > 1 && out.stride[0] < w.rows))
       NOT_TAKEN;
     dt = out.dtype;
-    if (x->rows > 1) ldy = out.stride[0];
+    if (x.rows > 1) ldy = out.stride[0];
   }
-  if (dt < 0 || !target(x->index, args[6], &stream)) NOT_TAKEN;
-  PyObject* y;
-  if (has_out) {
-    y = Py_NewRef(args[4]);
-  } else {
-    y = empty(2, x->rows, w->rows, args[3], x->device, &out.ptr);
-    if (!y) return nullptr;
-  }
+  if (dt < 0 || !target(x.index, args[6], &stream)) NOT_TAKEN;
+  at::Tensor y;
   const int32_t rc = launch([&] {
-    return lib.linear(reinterpret_cast<const void*>(x->codes_ptr), x->fmt,
-                      reinterpret_cast<const void*>(x->scales_ptr), (int32_t)x->rows,
-                      reinterpret_cast<const void*>(w->codes_ptr), w->fmt,
-                      reinterpret_cast<const void*>(w->scales_ptr), (int32_t)w->rows, (int32_t)w->K,
-                      reinterpret_cast<const float*>(bias.ptr), reinterpret_cast<void*>(out.ptr), dt,
-                      ldy, reinterpret_cast<int32_t*>(status.ptr), stream);
+    if (!has_out) {
+      y = empty({(int64_t)x.rows, (int64_t)w.rows}, scalar_type(dt), x.index);
+      out.ptr = y.data_ptr();
+    }
+    return lib.linear(reinterpret_cast<const void*>(x.codes_ptr), x.fmt,
+                      reinterpret_cast<const void*>(x.scales_ptr), (int32_t)x.rows,
+                      reinterpret_cast<const void*>(w.codes_ptr), w.fmt,
+                      reinterpret_cast<const void*>(w.scales_ptr), (int32_t)w.rows, (int32_t)w.K,
+                      static_cast<const float*>(bias.ptr), out.ptr, dt, ldy,
+                      static_cast<int32_t*>(status.ptr), stream);
   });
-  if (rc != STRATA_OK) {
-    Py_DECREF(y);
-    NOT_TAKEN;
-  }
-  return y;
+  if (rc != STRATA_OK) NOT_TAKEN;
+  return has_out ? Py_NewRef(args[4]) : THPVariable_Wrap(std::move(y));
 }
 
-// setup(addresses, torch.empty, torch.Tensor, Parameter, torch.device, current_device, current_stream,
-//       (float32, float16, bfloat16, uint8, int32), MXTensor, AddNorm)
+// setup(addresses, torch.Tensor, Parameter, MXTensor, AddNorm)
 PyObject* setup(PyObject*, PyObject* args) {
   unsigned long long f[4];
-  PyObject* o[8];
-  PyObject* t[5];
-  if (!PyArg_ParseTuple(args, "(KKKK)OOOOOO(OOOOO)OO", &f[0], &f[1], &f[2], &f[3], &o[0], &o[1],
-                        &o[2], &o[3], &o[4], &o[5], &t[0], &t[1], &t[2], &t[3], &t[4], &o[6], &o[7]))
+  PyObject* o[4];
+  if (!PyArg_ParseTuple(args, "(KKKK)OOOO", &f[0], &f[1], &f[2], &f[3], &o[0], &o[1], &o[2], &o[3]))
     return nullptr;
-  if (!PyType_Check(o[6]) || !PyType_IsSubtype((PyTypeObject*)o[6], matrix_type)) {
-    PyErr_SetString(PyExc_TypeError, "MXTensor must be a subclass of Matrix");
+  if (!PyType_Check(o[2]) || !PyType_IsSubtype((PyTypeObject*)o[2], matrix_type) ||
+      !PyType_Check(o[3]) || !PyType_IsSubtype((PyTypeObject*)o[3], &PyTuple_Type)) {
+    PyErr_SetString(PyExc_TypeError, "MXTensor must be a subclass of Matrix, AddNorm of tuple");
     return nullptr;
   }
   lib.quantize = reinterpret_cast<decltype(lib.quantize)>(f[0]);
   lib.dequantize = reinterpret_cast<decltype(lib.dequantize)>(f[1]);
   lib.add_rmsnorm = reinterpret_cast<decltype(lib.add_rmsnorm)>(f[2]);
   lib.linear = reinterpret_cast<decltype(lib.linear)>(f[3]);
-  PyObject** to[] = {&torch_empty,  &torch_tensor,   &torch_param,
-                     &torch_device, &current_device, &current_stream};
-  for (int i = 0; i < 6; ++i) Py_XSETREF(*to[i], Py_NewRef(o[i]));
-  for (int i = 0; i < 3; ++i) Py_XSETREF(dtypes[i], Py_NewRef(t[i]));
-  Py_XSETREF(uint8, Py_NewRef(t[3]));
-  Py_XSETREF(int32, Py_NewRef(t[4]));
-  Py_XSETREF(mx_type, reinterpret_cast<PyTypeObject*>(Py_NewRef(o[6])));
-  Py_XSETREF(add_norm, Py_NewRef(o[7]));
+  Py_XSETREF(torch_tensor, Py_NewRef(o[0]));
+  Py_XSETREF(torch_param, Py_NewRef(o[1]));
+  Py_XSETREF(mx_type, reinterpret_cast<PyTypeObject*>(Py_NewRef(o[2])));
+  Py_XSETREF(norm_type, reinterpret_cast<PyTypeObject*>(Py_NewRef(o[3])));
   Py_RETURN_NONE;
 }
 
+#define CALL(f) {#f, (PyCFunction)(void*)call<f>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
-    {"setup", setup, METH_VARARGS, "Hands over the library's functions and torch's."},
-    {"wrap", (PyCFunction)(void*)wrap, METH_FASTCALL, "MXTensor's fields; False where it does not take them."},
-    {"quantize", (PyCFunction)(void*)quantize, METH_FASTCALL, "mx_quantize, or None."},
-    {"dequantize", (PyCFunction)(void*)dequantize, METH_FASTCALL, "MXTensor.dequantize, or None."},
-    {"add_rmsnorm", (PyCFunction)(void*)add_rmsnorm, METH_FASTCALL, "add_rmsnorm, or None."},
-    {"linear", (PyCFunction)(void*)linear, METH_FASTCALL, "mx_linear, or None."},
+    {"setup", setup, METH_VARARGS, "Hands over the library's functions and mx.py's types."},
+    CALL(wrap),         // MXTensor's fields: True, or None
+    CALL(quantize),     // what mx.py's function of the name returns, or None
+    CALL(dequantize),
+    CALL(add_rmsnorm),
+    CALL(linear),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_mxcalls",
@@ -509,17 +499,12 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_mxcalls",
 }  // namespace
 
 PyMODINIT_FUNC PyInit__mxcalls(void) {
-  s_shape = PyUnicode_InternFromString("shape");
-  s_stride = PyUnicode_InternFromString("stride");
-  s_dtype = PyUnicode_InternFromString("dtype");
-  s_data_ptr = PyUnicode_InternFromString("data_ptr");
-  s_get_device = PyUnicode_InternFromString("get_device");
   s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-  s_cuda = PyUnicode_InternFromString("cuda");
-  kw_empty = Py_BuildValue("(ss)", "dtype", "device");
   PyObject* m = PyModule_Create(&module_def);
   PyObject* type = PyType_FromSpec(&matrix_spec);
   matrix_type = reinterpret_cast<PyTypeObject*>(type);
-  if (!m || !type || !kw_empty || PyModule_AddObject(m, "Matrix", type) < 0) return nullptr;
+  if (!m || !type || !s_cuda_stream || PyModule_AddObject(m, "Matrix", type) < 0 ||
+      PyModule_AddStringConstant(m, "torch_version", STRATA_TORCH) < 0)
+    return nullptr;
   return m;
 }

@@ -3,6 +3,7 @@
 Quantised codes and scales, and values read back, are compared bit for bit:
 the format determines them.  Tolerances elsewhere are counted in half steps
 (2^-8 for bf16, 2^-11 for fp16, 2^-24 for fp32) as each test derives."""
+import concurrent.futures
 import gc
 import sys
 
@@ -652,3 +653,52 @@ def test_native_calls_leave_refusals_to_python():
             (lambda: sm.mx_linear(q, q, out_dtype=torch.int32), TypeError, "dtype")):
         with pytest.raises(error, match=match):
             call()
+
+
+def test_native_calls_leave_dispatch_modes_to_python():
+    """A mode that watches torch's allocations sees those of these calls."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Seen(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            names.append(func.name())
+            return func(*args, **(kwargs or {}))
+
+    names = []
+    x = torch.randn(3, 64, device=DEV)
+    want = sm.mx_quantize(x, sm.MX_FP8)
+    with Seen():
+        got = sm.mx_quantize(x, sm.MX_FP8)
+    assert any(n.startswith("aten::empty") for n in names)
+    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+
+
+def test_native_calls_leave_tensors_without_memory_to_python():
+    sm.mx_quantize(torch.randn(3, 64, device=DEV), sm.MX_FP8)
+    with pytest.raises(RuntimeError):
+        torch.vmap(lambda r: sm.mx_quantize(r, sm.MX_FP8).codes)(torch.randn(2, 3, 64, device=DEV))
+
+
+def test_native_calls_out_of_memory():
+    x = torch.zeros(1, 4096, device=DEV).expand(1 << 26, 4096)  # its codes: 256 GiB
+    with pytest.raises(torch.OutOfMemoryError):
+        sm.mx_quantize(x, sm.MX_FP8)
+    assert (sm.mx_quantize(x[:3], sm.MX_FP8).codes == 0).all()
+
+
+def test_native_calls_of_several_threads():
+    g = gen(81)
+    xs = [torch.randn(5, 256, device=DEV, generator=g) for _ in range(4)]
+    w = sm.mx_quantize(torch.randn(70, 256, device=DEV, generator=g), sm.MX_FP4)
+
+    def calls(x):
+        n = sm.add_rmsnorm(x, x, fmt=sm.MX_FP8, out_dtype=torch.float16)
+        return n.residual, n.out, sm.mx_linear(n.mx, w), n.mx.dequantize()
+
+    want = [calls(x) for x in xs]
+    with concurrent.futures.ThreadPoolExecutor(4) as pool:
+        gots = list(pool.map(lambda i: [calls(xs[i]) for _ in range(100)], range(4)))
+    torch.cuda.synchronize()
+    for i, got in enumerate(gots):
+        for once in got:
+            assert all(torch.equal(a, b) for a, b in zip(once, want[i]))
