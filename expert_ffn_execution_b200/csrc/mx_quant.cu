@@ -137,6 +137,11 @@ mx_quantize_kernel(const __grid_constant__ Jobs<MxQuantArgs> jobs) {
   Place p[kQUnroll];
   places_of(jobs, j, p);
   pdl_wait_prior();
+  // Scales in tiles are the product's operand: its CTAs set up while this grid
+  // runs and wait for its end before they read (T = 1, N = 10240, K = 2560,
+  // 8x4 bits, quantised and multiplied: 8.9 us without, 8.2 us).  Experts'
+  // blobs may be read before a wait: nothing is released for them.
+  if (a.layout == STRATA_MX_TILES) pdl_trigger();
   Raw8<DT> raw[kQUnroll][2];
 #pragma unroll
   for (int u = 0; u < kQUnroll; ++u) {

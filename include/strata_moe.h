@@ -387,7 +387,8 @@ STRATA_API int32_t moe_layer_forward(const float* x, int32_t T, const uint16_t* 
  * e = s + 127, and an element is x / 2^s rounded to nearest even, saturated
  * at 6 (FP4) or 448 (FP8), the sign of zero kept.  A block that holds an Inf
  * or NaN gets e = 255 and codes 0.  The result is determined bit for bit.
- * None of these calls releases its dependents early, so their outputs can be
+ * Of these calls moe_mx_quantize to tiles alone releases its dependents early
+ * (when the grid before it has ended), so the others' outputs can be
  * moe_combine's inv, topk_w or residual. */
 #define STRATA_MX_FP4 1
 #define STRATA_MX_FP8 2

@@ -480,6 +480,29 @@ def test_two_graphs_and_a_side_stream():
             assert torch.equal(r, wr) and torch.equal(o, wo)
 
 
+@pytest.mark.parametrize("rows", [1, 4096])
+def test_a_residual_behind_an_early_release(rows):
+    """moe_combine reads its residual before it waits, and the quantiser lets
+    it start early: what the norm before both wrote is there."""
+    T, H = 64, 2560
+    big = torch.randn(rows, 1024, device=DEV, generator=gen(60))
+    codes = sm.mx_quantize(big, sm.MX_FP8).codes.clone()
+    y = torch.zeros(T, H, device=DEV)
+    inv = torch.arange(T, dtype=torch.int32, device=DEV)
+    w = torch.ones(T, 1, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, acc = torch.empty(T, H, dtype=torch.bfloat16, device=DEV), torch.empty(T, H, device=DEV)
+    r = torch.zeros(T, H, device=DEV)
+    for i in range(20):
+        x = torch.randn(T, H, device=DEV, generator=gen(61 + i))
+        torch.cuda.synchronize()
+        sm.add_rmsnorm(x, x, fmt=sm.MX_FP8, residual_out=r)
+        q = sm.mx_quantize(big, sm.MX_FP8)
+        sm.moe_combine(y, sm.DTYPE_F32, inv, w, None, sm.DTYPE_F32, r, T, 1, H, out, acc, status)
+        assert torch.equal(acc, x + x) and torch.equal(q.codes, codes)
+    assert sm.strata_read_status(status) == 0
+
+
 @pytest.mark.parametrize("T", [4, 48])
 def test_packed_experts_in_the_layer(T):
     """bf16 weights -> blobs -> the MoE layer -> the norm after it -> a
