@@ -3,12 +3,15 @@
 //   r = x + delta;  h = r / sqrt(mean r^2 + eps) * gain;
 //   residual_out = r;  out = round(h);  codes, scales = MX(h).
 //
-// One CTA a row, the row in registers between the sum of squares and the
-// output, so every input is read once and every output written once: bound by
-// HBM for many rows (T = 8192, H = 4096, fp32 + bf16 to bf16 and FP8: 66.9 us,
-// 6.5 TB/s), by the launch and one load-reduce-store chain for few.  CTAs that
-// take rows in turn, with the next rows copied ahead, are slower (98 us): a
-// row's two reductions are the wait, and many CTAs hide it better than a few.
+// A row is one CTA's, or one or two warps' of a CTA of 128 threads, and stays
+// in registers between the sum of squares and the output, so every input is
+// read once and every output written once: bound by HBM for many rows (T =
+// 8192, H = 4096, fp32 + bf16 to bf16 and FP8: 66.9 us, 6.5 TB/s), by
+// instructions where a row is only read and its codes written (126 a group of
+// 8 elements and warp; T = 5859, H = 4096, bf16 to FP4: 19.8 us), by the
+// launch and one load-reduce-store chain for few.  CTAs that take rows in
+// turn, with the next rows copied ahead, are slower (98 us for 66.9): a row's
+// two reductions are the wait, and many CTAs hide it better than a few.
 //
 // A thread's up to 32 squares are summed in fp32, the threads' sums in fp64
 // (fixed order: warp butterfly, warp partials), which leaves the mean to one
@@ -49,105 +52,98 @@ STRATA_DEVFN void store8_as(void* p, int dt, int64_t i, const float (&v)[8]) {
     store8<STRATA_DTYPE_BF16>(reinterpret_cast<uint16_t*>(p) + i, v);
 }
 
-// VPT groups of 8 elements a thread: group threadIdx.x + blockDim.x * j.  XT,
-// DT: dtypes of x and delta (DT < 0: no delta).
+// A group of 8 as codes, and its block's scale byte (four adjacent lanes hold
+// a block).
+template <int FMT>
+STRATA_DEVFN void put_mx(const AddNormArgs& a, const float (&h)[8], int64_t group, uint8_t* scale,
+                         bool some) {
+  uint32_t m = max_bits8(h);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t e = mx_scale_of<FMT>(m);
+  const uint2 c = mx_encode8<FMT>(h, e);
+  if (!some) return;
+  if constexpr (FMT == STRATA_MX_FP4)
+    reinterpret_cast<uint32_t*>(a.codes)[group] = c.x;
+  else
+    reinterpret_cast<uint2*>(a.codes)[group] = c;
+  if (threadIdx.x % 4 == 0) *scale = (uint8_t)e;
+}
+
+// A row is blockDim.x threads', VPT groups of 8 elements each: group threadIdx.x
+// + blockDim.x * j; a CTA has blockDim.y rows.  XT, DT: dtypes of x and delta
+// (DT < 0: no delta).
 template <int XT, int DT, int VPT>
 __global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a) {
   __shared__ double red[kNMaxThreads / 32];
   const int tid = threadIdx.x, nth = blockDim.x;
-  const int G = a.H / 8;
-  const int kt = (a.H + 127) / 128;
-  const int row = blockIdx.x;
+  const int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const int G = row < a.T ? a.H / 8 : 0;
   pdl_wait_prior();
-  if (row < a.T) {
-    const int64_t base = (int64_t)row * a.H;
-    float r[VPT][8];
-    float ss = 0.f;
-    load_groups<XT>(a.x, base, G, r);
-    if constexpr (DT >= 0) {
-      float d[VPT][8];
-      load_groups<DT>(a.delta, base, G, d);
+  const int64_t base = (int64_t)row * a.H;
+  float r[VPT][8];
+  float even = 0.f, odd = 0.f;  // sums of squares
+  load_groups<XT>(a.x, base, G, r);
+  if constexpr (DT >= 0) {
+    float d[VPT][8];
+    load_groups<DT>(a.delta, base, G, d);
 #pragma unroll
-      for (int j = 0; j < VPT; ++j)
+    for (int j = 0; j < VPT; ++j) add8(r[j], d[j]);
+  }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[j][i] += d[j][i];
-    }
+  for (int j = 0; j < VPT; ++j) {
+    const int g = tid + nth * j;
+    if (a.residual_out && g < G)
+      store8<XT>(reinterpret_cast<uint8_t*>(a.residual_out) +
+                     (base + 8 * g) * (XT == STRATA_DTYPE_F32 ? 4 : 2),
+                 r[j]);
+    squares8(r[j], even, odd);
+  }
+  double sum = (double)even + odd;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int g = tid + nth * j;
-      if (a.residual_out && g < G)
-        store8<XT>(reinterpret_cast<uint8_t*>(a.residual_out) +
-                       (base + 8 * g) * (XT == STRATA_DTYPE_F32 ? 4 : 2),
-                   r[j]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(r[j][i], r[j][i], ss);
-    }
-    double sum = ss;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((tid & 31) == 0) red[tid >> 5] = sum;
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (nth > 32) {
+    double* part = red + threadIdx.y * (nth / 32);
+    if ((tid & 31) == 0) part[tid >> 5] = sum;
     __syncthreads();
-    sum = (tid & 31) < nth / 32 ? red[tid & 31] : 0.;
+    sum = (tid & 31) < nth / 32 ? part[tid & 31] : 0.;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     sum = __shfl_sync(0xffffffffu, sum, 0);
-    const float inv = rsqrtf((float)sum * (1.0f / (float)a.H) + a.eps);
+  }
+  const int kt = (a.H + 127) / 128;
+  const bool tiles = a.fmt && a.layout == STRATA_MX_TILES;
+  uint8_t* const scales = a.scales + (tiles ? mx_tile_row(row, kt) : base / kMxBlock);
+  const float inv = rsqrtf((float)sum * a.inv_H + a.eps);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int g = tid + nth * j;
-      float h[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = r[j][i] * inv;
-      if (a.gain && g < G) {
-        float w[8];
-        load8<STRATA_DTYPE_F32>(a.gain + 8 * g, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] *= w[i];
-      }
-      if (a.out && g < G) store8_as(a.out, a.out_dtype, base + 8 * g, h);
-      if (a.fmt) {
-        // four adjacent lanes hold a block of 32
-        uint32_t m = max_bits8(h);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        uint2 c;
-        uint32_t e;
-        if (a.fmt == STRATA_MX_FP4) {
-          e = mx_scale_of<STRATA_MX_FP4>(m);
-          c = mx_encode8<STRATA_MX_FP4>(h, e);
-        } else {
-          e = mx_scale_of<STRATA_MX_FP8>(m);
-          c = mx_encode8<STRATA_MX_FP8>(h, e);
-        }
-        if (g < G) {
-          if (a.fmt == STRATA_MX_FP4)
-            reinterpret_cast<uint32_t*>(a.codes)[base / 8 + g] = c.x;
-          else
-            reinterpret_cast<uint2*>(a.codes)[base / 8 + g] = c;
-          if ((tid & 3) == 0) {
-            if (a.layout == STRATA_MX_TILES)
-              a.scales[mx_tile_byte(row, g / 4, kt)] = (uint8_t)e;
-            else
-              a.scales[(base + 8 * g) / kMxBlock] = (uint8_t)e;
-          }
-        }
-      }
+  for (int j = 0; j < VPT; ++j) {
+    const int g = tid + nth * j;
+    float h[8];
+    scale8(r[j], inv, h);
+    if (a.gain && g < G) {
+      float w[8];
+      load8<STRATA_DTYPE_F32>(a.gain + 8 * g, w);
+      mul8(h, w, h);
     }
+    if (a.out && g < G) store8_as(a.out, a.out_dtype, base + 8 * g, h);
+    uint8_t* const scale = scales + (tiles ? mx_tile_block(g / 4) : g / 4);
+    if (a.fmt == STRATA_MX_FP4)
+      put_mx<STRATA_MX_FP4>(a, h, base / 8 + g, scale, g < G);
+    else if (a.fmt == STRATA_MX_FP8)
+      put_mx<STRATA_MX_FP8>(a, h, base / 8 + g, scale, g < G);
   }
   // padding of the scale tiles: the last blocks of every row, and the rows
-  // behind the last
-  if (a.fmt && a.layout == STRATA_MX_TILES) {
-    for (int b = (row < a.T ? a.H / kMxBlock : 0) + tid; b < kt * kMxTileBlocks; b += nth)
-      a.scales[mx_tile_byte(row, b, kt)] = 0;
-  }
+  // behind the last (the grid ends with the last tile's)
+  if (tiles)
+    for (int b = G / 4 + tid; b < kt * kMxTileBlocks; b += nth) scales[mx_tile_block(b)] = 0;
 }
 
 template <int XT, int DT, int VPT>
-cudaError_t launch_norm(const AddNormArgs& a, int rows, int threads, cudaStream_t st) {
+cudaError_t launch_norm(const AddNormArgs& a, int rows, dim3 block, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(rows);
-  cfg.blockDim = dim3(threads);
+  cfg.gridDim = dim3((rows + block.y - 1) / block.y);
+  cfg.blockDim = block;
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -157,21 +153,21 @@ cudaError_t launch_norm(const AddNormArgs& a, int rows, int threads, cudaStream_
 }
 
 template <int XT, int VPT>
-cudaError_t launch_norm_d(const AddNormArgs& a, int rows, int threads, cudaStream_t st) {
-  if (!a.delta) return launch_norm<XT, -1, VPT>(a, rows, threads, st);
+cudaError_t launch_norm_d(const AddNormArgs& a, int rows, dim3 block, cudaStream_t st) {
+  if (!a.delta) return launch_norm<XT, -1, VPT>(a, rows, block, st);
   if (a.delta_dtype == STRATA_DTYPE_F32)
-    return launch_norm<XT, STRATA_DTYPE_F32, VPT>(a, rows, threads, st);
+    return launch_norm<XT, STRATA_DTYPE_F32, VPT>(a, rows, block, st);
   if (a.delta_dtype == STRATA_DTYPE_F16)
-    return launch_norm<XT, STRATA_DTYPE_F16, VPT>(a, rows, threads, st);
-  return launch_norm<XT, STRATA_DTYPE_BF16, VPT>(a, rows, threads, st);
+    return launch_norm<XT, STRATA_DTYPE_F16, VPT>(a, rows, block, st);
+  return launch_norm<XT, STRATA_DTYPE_BF16, VPT>(a, rows, block, st);
 }
 template <int VPT>
-cudaError_t launch_norm_x(const AddNormArgs& a, int rows, int threads, cudaStream_t st) {
+cudaError_t launch_norm_x(const AddNormArgs& a, int rows, dim3 block, cudaStream_t st) {
   if (a.x_dtype == STRATA_DTYPE_F32)
-    return launch_norm_d<STRATA_DTYPE_F32, VPT>(a, rows, threads, st);
+    return launch_norm_d<STRATA_DTYPE_F32, VPT>(a, rows, block, st);
   if (a.x_dtype == STRATA_DTYPE_F16)
-    return launch_norm_d<STRATA_DTYPE_F16, VPT>(a, rows, threads, st);
-  return launch_norm_d<STRATA_DTYPE_BF16, VPT>(a, rows, threads, st);
+    return launch_norm_d<STRATA_DTYPE_F16, VPT>(a, rows, block, st);
+  return launch_norm_d<STRATA_DTYPE_BF16, VPT>(a, rows, block, st);
 }
 
 }  // namespace
@@ -180,16 +176,34 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t st) {
   const int rows = a.fmt && a.layout == STRATA_MX_TILES
                        ? (int)(mx_ceil(a.T, kMxTileRows) * kMxTileRows)
                        : a.T;
-  // One group a thread, or two (32 bytes of a 16-bit x) where there are rows
-  // enough to fill the SMs: T = 4096, H = 4096, bf16 to FP4 24.4 us with one,
-  // 21.5 with two; T = 16: 2.5 and 2.8; fp32 rows 66.9 and 67.8 (T = 8192).
   const int G = a.H / 8;
-  int vpt = a.x_dtype != STRATA_DTYPE_F32 && a.T > 148 ? 2 : 1;
+  const int64_t groups = (int64_t)a.T * G;
+  // Groups a thread: one where that leaves SMs half empty (a thread's chain is
+  // the time: T = 234, H = 1024, bf16 to FP4 2.2 us, with two 2.4) and for
+  // rows of one warp; else two, which share a thread's fixed part (T = 2343:
+  // 4.0 and 3.4 us).  With the SMs filled several times over, rows that are
+  // only read are bound by instructions, four save more of them (T = 23437:
+  // 24.1, 20.0 and 18.0 us with one, two and four), and fp32 rows with a
+  // delta by HBM (T = 5859, H = 4096: 48.7, 49.2 and 52.7 us).
+  const int64_t filled = (int64_t)148 * 64 * 32;
+  int vpt = 1;
+  if (G > 32 && groups > filled / 2) vpt = 2;
+  if (vpt == 2 && groups > 4 * filled)
+    vpt = !a.delta ? (G > 64 ? 4 : 2) : a.x_dtype == STRATA_DTYPE_F32 ? 1 : 2;
+  // threads of a row, whole warps; not an eighth more idle ones than with half
+  // of the groups (H = 1536, four groups: 22.2 us, two: 20 us)
+  auto threads_of = [&](int v) { return ((G + v - 1) / v + 31) & ~31; };
+  while (vpt > 1 && 8 * vpt * threads_of(vpt) > 9 * (vpt / 2) * threads_of(vpt / 2)) vpt /= 2;
   while (G > vpt * kNMaxThreads) vpt *= 2;
-  const int threads = (((G + vpt - 1) / vpt) + 31) & ~31;
-  if (vpt == 1) return launch_norm_x<1>(a, rows, threads, st);
-  if (vpt == 2) return launch_norm_x<2>(a, rows, threads, st);
-  return launch_norm_x<4>(a, rows, threads, st);
+  const int threads = threads_of(vpt);
+  // up to 128 threads a CTA, then a CTA a row (T = 93750, H = 256, bf16 to
+  // FP4: 22 us with four rows a CTA, 51 with one)
+  int per = 1;
+  while (2 * per * threads <= 128) per *= 2;
+  const dim3 block(threads, per);
+  if (vpt == 1) return launch_norm_x<1>(a, rows, block, st);
+  if (vpt == 2) return launch_norm_x<2>(a, rows, block, st);
+  return launch_norm_x<4>(a, rows, block, st);
 }
 
 }  // namespace strata

@@ -27,10 +27,17 @@ __host__ __device__ inline int64_t mx_scale_plane(int64_t rows, int64_t K, int l
              ? mx_ceil(rows, kMxTileRows) * mx_ceil(K, kMxTileBlocks * kMxBlock) * kMxTileBytes
              : rows * (K / kMxBlock);
 }
-// Byte of (row, block) in a plane of `kt` scale tiles a row of tiles.
-__host__ __device__ inline int64_t mx_tile_byte(int row, int block, int kt) {
-  return ((int64_t)(row / kMxTileRows) * kt + block / kMxTileBlocks) * kMxTileBytes +
-         (row % 32) * 16 + (row / 32 % 4) * 4 + block % kMxTileBlocks;
+// Byte of (row, block) in a plane of `kt` scale tiles a row of tiles: the
+// row's part and the block's.
+__host__ __device__ inline int64_t mx_tile_row(uint32_t row, uint32_t kt) {
+  return (int64_t)((uint64_t)(row / kMxTileRows) * kt * kMxTileBytes) +
+         (row % 32 * 16 + row / 32 % 4 * 4);
+}
+__host__ __device__ inline int64_t mx_tile_block(uint32_t block) {
+  return (int64_t)(block / kMxTileBlocks) * kMxTileBytes + block % kMxTileBlocks;
+}
+__host__ __device__ inline int64_t mx_tile_byte(uint32_t row, uint32_t block, uint32_t kt) {
+  return mx_tile_row(row, kt) + mx_tile_block(block);
 }
 
 // ---------------------------------------------------------------- 8 elements
@@ -76,6 +83,40 @@ STRATA_DEVFN void load8(const void* p, float (&v)[8]) {
   r.values(v);
 }
 
+// Eight products, two an instruction; c may be a.
+STRATA_DEVFN void mul8(const float (&a)[8], const float (&b)[8], float (&c)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(c[i]), "=f"(c[i + 1])
+        : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+}
+STRATA_DEVFN void scale8(const float (&a)[8], float s, float (&c)[8]) {
+  const float b[8] = {s, s, s, s, s, s, s, s};
+  mul8(a, b, c);
+}
+// a += b, and two running sums of squares.
+STRATA_DEVFN void add8(float (&a)[8], const float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a[i]), "+f"(a[i + 1])
+        : "f"(b[i]), "f"(b[i + 1]));
+}
+STRATA_DEVFN void squares8(const float (&a)[8], float& even, float& odd) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("{\n\t.reg .b64 a, s;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 s, {%0, %1};\n\t"
+        "fma.rn.f32x2 s, a, a, s;\n\tmov.b64 {%0, %1}, s;\n\t}"
+        : "+f"(even), "+f"(odd)
+        : "f"(a[i]), "f"(a[i + 1]));
+}
+
 // Two values rounded to nearest even in the 16-bit type DT, first one low.
 template <int DT>
 STRATA_DEVFN uint32_t pack2(float a, float b) {
@@ -117,6 +158,8 @@ template <int FMT>
 STRATA_DEVFN uint2 mx_encode8(const float (&v)[8], uint32_t e) {
   uint2 codes = make_uint2(0u, 0u);
   const float s = __uint_as_float((254u - e) << 23);  // not used for e = 255
+  float x[8];
+  scale8(v, s, x);
   // the conversions' pairs are joined as registers of 8 and 16 bits (joined by
   // shifts, 52M bf16 to MXFP4 took 24.2 us for 22.6)
   if constexpr (FMT == STRATA_MX_FP4) {
@@ -127,8 +170,8 @@ STRATA_DEVFN uint2 mx_encode8(const float (&v)[8], uint32_t e) {
         "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
         "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(codes.x)
-        : "f"(v[0] * s), "f"(v[1] * s), "f"(v[2] * s), "f"(v[3] * s), "f"(v[4] * s),
-          "f"(v[5] * s), "f"(v[6] * s), "f"(v[7] * s));
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]),
+          "f"(x[5]), "f"(x[6]), "f"(x[7]));
   } else {
     asm("{\n\t.reg .b16 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 a, %3, %2;\n\t"
@@ -138,17 +181,21 @@ STRATA_DEVFN uint2 mx_encode8(const float (&v)[8], uint32_t e) {
         "mov.b32 %0, {a, b};\n\t"
         "mov.b32 %1, {c, d};\n\t}"
         : "=r"(codes.x), "=r"(codes.y)
-        : "f"(v[0] * s), "f"(v[1] * s), "f"(v[2] * s), "f"(v[3] * s), "f"(v[4] * s),
-          "f"(v[5] * s), "f"(v[6] * s), "f"(v[7] * s));
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]),
+          "f"(x[5]), "f"(x[6]), "f"(x[7]));
   }
   return e == 255u ? make_uint2(0u, 0u) : codes;
 }
+STRATA_DEVFN float max3(float a, float b, float c) {  // NaN where one is
+  float m;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+// Bits of the largest magnitude; above every number's where one is NaN.
 STRATA_DEVFN uint32_t max_bits8(const float (&v)[8]) {
-  uint32_t b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(v[i]) & 0x7fffffffu;
-  return __vimax3_u32(__vimax3_u32(b[0], b[1], b[2]), __vimax3_u32(b[3], b[4], b[5]),
-                      max(b[6], b[7]));
+  const float m = max3(fabsf(v[0]), fabsf(v[1]), fabsf(v[2]));
+  const float n = max3(fabsf(v[3]), fabsf(v[4]), fabsf(v[5]));
+  return __float_as_uint(max3(max3(m, n, fabsf(v[6])), fabsf(v[7]), 0.f));
 }
 
 template <int DT>
@@ -176,7 +223,6 @@ STRATA_DEVFN float mx_scale_value(uint32_t e) {
 // step under the smallest scale.
 template <int FMT>
 STRATA_DEVFN void mx_decode8(uint2 codes, uint32_t e, float (&v)[8]) {
-  const float s = mx_scale_value(e);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     __half2_raw h;
@@ -187,9 +233,10 @@ STRATA_DEVFN void mx_decode8(uint2 codes, uint32_t e, float (&v)[8]) {
       h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (i & 1))), __NV_E4M3);
     }
     const float2 f = __half22float2(__half2(h));
-    v[2 * i] = f.x * s;
-    v[2 * i + 1] = f.y * s;
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
   }
+  scale8(v, mx_scale_value(e), v);
 }
 
 // ---------------------------------------------------------------- interfaces
@@ -231,7 +278,7 @@ struct AddNormArgs {
   int delta_dtype;
   const float* gain;  // or nullptr
   int T, H;
-  float eps;
+  float eps, inv_H;
   void* residual_out;  // dtype of x, or nullptr
   void* out;           // or nullptr
   int out_dtype;

@@ -218,6 +218,26 @@ def test_norm_quantised(T, H, fmt, layout):
     assert only.out is None and torch.equal(only.mx.codes, n.mx.codes) and torch.equal(only.mx.scales, n.mx.scales)
 
 
+@pytest.mark.parametrize("T,H", [(4099, 128), (5003, 256), (1203, 1056), (9481, 1024), (9481, 1536), (150, 16384)])
+@pytest.mark.parametrize("xt,dt", [(torch.float32, torch.bfloat16), (torch.bfloat16, torch.bfloat16),
+                                   (torch.float32, None), (torch.bfloat16, None)])
+def test_norm_of_many_rows(xt, dt, T, H):
+    """Rows that share a CTA, and several groups a thread."""
+    g = gen(T + H)
+    x = torch.randn(T, H, device=DEV, generator=g).to(xt)
+    delta = None if dt is None else torch.randn(T, H, device=DEV, generator=g).to(dt)
+    gain = 1 + 0.1 * torch.randn(H, device=DEV, generator=g)
+    n = sm.add_rmsnorm(x, delta, gain, 1e-6, out_dtype=torch.float32, fmt=sm.MX_FP8)
+    q = sm.mx_quantize(n.out, sm.MX_FP8)
+    assert torch.equal(n.mx.codes, q.codes) and torch.equal(n.mx.scales, q.scales)
+    r = size = x.double()
+    if delta is not None:
+        assert torch.equal(n.residual, (x.float() + delta.float()).to(xt))
+        r, size = r + delta.double(), r.abs() + delta.double().abs()
+    k = gain.double() / (r.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt()
+    assert ((n.out.double() - r * k).abs() <= (H_REL + 2.0 ** -24) * (size * k).abs()).all()
+
+
 def test_norm_in_place_and_zero_rows():
     x = torch.randn(6, 256, device=DEV, generator=gen(5))
     x[2] = 0
