@@ -7,7 +7,7 @@
 // tokens x 256 features, each CTA loading 128 rows of both and holding 128
 // tokens x 256 features of the sums.  T = 8192, N = 16384, K = 4096, 4x4 bits:
 // 431 us with 128 x 128 tiles of one CTA, 188 us (5.9 PFLOP/s) here; N =
-// 10240, K = 2560, 8x4 bits: 304 and 146 us (2.9 PFLOP/s); the tensor pipe is
+// 10240, K = 2560, 8x4 bits: 304 and 147 us (2.9 PFLOP/s); the tensor pipe is
 // active for 74 and 79 % of the cycles.  The order of the tiles makes no
 // difference (operands of this size stay in L2).
 //
@@ -83,7 +83,7 @@ STRATA_DEVFN void store_rows(const uint8_t* buf, uint8_t* y, int64_t pitch, int 
 // to how it lies in 16-byte pieces of memory, whole pieces are stored as such
 // and the (up to two) others element by element.  `left` bytes of a row are
 // y's.  Element by element throughout, the stores took longer than the MMAs:
-// T = 1452, N = 25295, K = 640, 4x4 bits 49 us, now 32 us, and 24 us with N =
+// T = 1452, N = 25295, K = 640, 4x4 bits 49 us, now 35 us, and 31 us with N =
 // 25296, whose rows are on 16-byte boundaries.
 template <int EL>
 STRATA_DEVFN void store_shifted(uint32_t* buf, const uint32_t* w, uint8_t* y, int64_t pitch,

@@ -13,10 +13,10 @@
 // which bounds it by HBM up to a few hundred tokens.  A CTA owns 128 features
 // x NT tokens; where there are fewer tiles than SMs the K axis is split over a
 // cluster of up to 8 CTAs, and every CTA joins the sums of some of the tokens
-// in rank order.  Joining is a matter of round trips: T = 4, N = 2560, K =
-// 2560, 8x4 bits takes 5.2 us when the sums are fetched, 16 bytes at a time,
-// behind a barrier that orders memory, and 4.5 us now that each CTA sends a
-// rank its tokens by one bulk copy that counts on the receiver's barrier.
+// in rank order.  Joining is a matter of round trips: with T = 4, N = 2560, K =
+// 2560, 8x4 bits, fetching the sums 16 bytes at a time behind a barrier that
+// orders memory took 5.2 us, and 4.5 us once each CTA sent a rank its tokens
+// by one bulk copy that counts on the receiver's barrier (4.0 us now).
 #include <algorithm>
 #include <cmath>
 
@@ -347,7 +347,8 @@ cudaError_t launch_linear(const MxLinearArgs& a, int splits, cudaStream_t st) {
   const bool split = splits > 1;
   const int lg = splits == 8 ? 3 : splits == 4 ? 2 : splits == 2 ? 1 : 0;
   // Clusters of 4 and 8 do not fill every SM of a GPC: at one CTA an SM some
-  // would wait for a second turn (N = 1024, K = 4096, T = 256: 14 us for 9).
+  // would wait for a second turn (T = 4, N = 2304, K = 8192, 8 ranks: 10.2 us
+  // for 6.4).
   const bool alone = splits <= 2 && (int64_t)tn * tt * splits <= a.num_sms;
   const int S = C::stages(alone ? C::kAlone : C::kShared, split);
   auto kern = mx_linear_kernel<XF, WF, NT>;
@@ -373,8 +374,8 @@ cudaError_t launch_linear(const MxLinearArgs& a, int splits, cudaStream_t st) {
 // Tokens a tile and ranks a tile, by what they cost in units of the 0.2 us
 // that a stage of 128 weight rows and 16 token rows takes its SM (2.5 cycles a
 // 128-byte row, whichever CTA it belongs to).  Measured, T = 4, 8x4 bits, with
-// 1, 2, 4 and 8 ranks: N = 2560, K = 8192 15.4, 9.8, 6.6 and 6.2 us; N = 1024,
-// K = 2560 6.7, 5.4, 4.5 and 4.2; N = 8192, K = 2048 6.0, 5.3 and 5.6.
+// 1, 2, 4 and 8 ranks: N = 2560, K = 8192 15.9, 10.1, 7.5 and 6.7 us; N = 1024,
+// K = 2560 6.6, 5.0, 4.0 and 3.6; N = 8192, K = 2048 6.5, 5.9 and 5.5.
 struct LinPlan {
   int nt, splits;
 };
@@ -410,8 +411,8 @@ template <int XF, int WF>
 cudaError_t launch_linear_t(const MxLinearArgs& a, cudaStream_t st) {
   // Past 128 tokens these tiles are taken while every SM gets at most one of
   // 128 x 128; beyond that the pairs' 256 x 256 tiles, with half of the
-  // copies, win.  K = 4096, 8x4 bits, N = 4096: 12.0 us here against 13.9 at
-  // T = 256; N = 16384: 21.4 against 16.5.
+  // copies, win.  T = 256, K = 4096, 8x4 bits, N = 4096: 12.1 us here against
+  // 15.5; N = 16384: 23.5 against 17.2.
   if (a.T > 128 && mx_ceil(a.T, 128) * mx_ceil(a.N, kLM) > a.num_sms) return launch_mx_gemm(a, st);
   const LinPlan p = plan_linear(a.T, a.N, a.K, XF == STRATA_MX_FP4 && WF == STRATA_MX_FP4, a.num_sms);
   if (p.nt == 16) return launch_linear<XF, WF, 16>(a, p.splits, st);

@@ -10,7 +10,8 @@
 // Matrix, row and column of the first come from its flat index by division,
 // those of the next, and their offsets, by adding.  8192 x 4096 bf16 to FP8:
 // 36 us with 8 elements and three divisions a piece, 24 us without the
-// divisions, 18 us (5.7 TB/s) with 16 elements and added offsets.
+// divisions, 18 us with 16 elements and added offsets, 17 us (6.0 TB/s) with
+// products two an instruction and tile offsets in unsigned arithmetic.
 #include "mx.cuh"
 #include "tc05.cuh"
 
