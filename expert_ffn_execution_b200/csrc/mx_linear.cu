@@ -371,34 +371,45 @@ cudaError_t launch_linear(const MxLinearArgs& a, int splits, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, wmap, xmap, a, lg, S);
 }
 
-// Tokens a tile and ranks a tile, by what they cost in units of the 0.2 us
-// that a stage of 128 weight rows and 16 token rows takes its SM (2.5 cycles a
-// 128-byte row, whichever CTA it belongs to).  Measured, T = 4, 8x4 bits, with
-// 1, 2, 4 and 8 ranks: N = 2560, K = 8192 15.9, 10.1, 7.5 and 6.7 us; N = 1024,
-// K = 2560 6.6, 5.0, 4.0 and 3.6; N = 8192, K = 2048 6.5, 5.9 and 5.5.
+// The form of a call, by what it costs in units of the 0.2 us that a stage of
+// 128 weight rows and 16 token rows takes its SM (2.5 cycles a 128-byte row,
+// whichever CTA it belongs to; the 8-bit operands' instructions hide behind
+// that, four bits' half as many stages take 1.9).  The factors are fitted to
+// every form's time on 788 shapes (1 to 1100 tokens, N to 24000, K to 8192,
+// all three pairs of formats): this takes the best form or one within 8 % of
+// it for 779, on average within 0.4 %.  Measured, T = 4, 8x4 bits, with 1, 2,
+// 4 and 8 ranks: N = 2560, K = 8192 15.9, 10.1, 7.5 and 6.7 us; N = 8192, K =
+// 2048 6.5, 5.9 and 5.5 with 1, 2 and 4.  T = 256, K = 4096, N = 4096: 11.9 us
+// in tiles of 64 tokens, 15.5 in the pairs' tiles; N = 16384: 23.5 in tiles of
+// 128, 17.2 in the pairs'.
 struct LinPlan {
-  int nt, splits;
+  int nt, splits;  // tokens a tile, 0: the pairs' tiles; ranks a tile
 };
 LinPlan plan_linear(int T, int N, int K, bool f4, int num_sms) {
   // Tiles of 16 and 32 tokens are for calls with one: a tile starts at a
   // multiple of 64 (its scales at a tensor-memory column of their own).
   const int lo = T <= 16 ? 16 : T <= 32 ? 32 : 64, hi = T <= 64 ? lo : 128;
   const int chunks = (int)mx_ceil(K, f4 ? 256 : 128);
-  LinPlan best = {lo, 1};
-  double least = 0;
+  LinPlan best = {0, 1};
+  double least = INFINITY;
+  if (T > 64) {
+    const double rounds = (double)mx_ceil(mx_ceil(T, 256) * mx_ceil(N, 256), num_sms / 2);
+    least = 7.5 + rounds * (chunks * (f4 ? 3.2 : 2.0) + 4);
+  }
   for (int nt = lo; nt <= hi; nt *= 2) {
     const int64_t tiles = mx_ceil(N, kLM) * mx_ceil(T, nt);
+    if (T > 64 && tiles > 5 * num_sms) continue;  // (past what was fitted)
     for (int s = 1; s <= 8; s *= 2) {
       const int64_t ctas = tiles * s;
       // (the sums of 128 tokens twice over leave no room for a second CTA)
       if (s > 1 && (nt == 128 || ctas > 2 * num_sms || chunks < 2 * s)) break;
       const double full = (double)ctas / num_sms;
       const double busy = full <= 1 ? 1 : (full + std::ceil(full)) / 2;
-      const double stage = (kLM + nt) / 144.0 * (f4 ? 1.25 : 1.0);
-      const double join = s == 1 ? 0 : (1.5 + 0.11 * nt) * (s == 2 ? 1 : s == 4 ? 1.25 : 1.4) +
-                                           (s == 8 && full > 1 ? 4 : 0);
-      const double cost = mx_ceil(chunks, s) * stage * busy + join + nt / 16.0;
-      if ((nt == lo && s == 1) || cost < least) {
+      const double stage = (kLM + nt) / 144.0 * (f4 ? 1.9 : 1.0);
+      const double join =
+          s == 1 ? 0 : (0.45 + 0.09 * nt) * (s == 2 ? 1 : 0.8) + (s == 8 && full > 1 ? 2 : 0);
+      const double cost = mx_ceil(chunks, s) * stage * busy + join + 0.11 * nt;
+      if (cost < least) {
         least = cost;
         best = {nt, s};
       }
@@ -409,16 +420,14 @@ LinPlan plan_linear(int T, int N, int K, bool f4, int num_sms) {
 
 template <int XF, int WF>
 cudaError_t launch_linear_t(const MxLinearArgs& a, cudaStream_t st) {
-  // Past 128 tokens these tiles are taken while every SM gets at most one of
-  // 128 x 128; beyond that the pairs' 256 x 256 tiles, with half of the
-  // copies, win.  T = 256, K = 4096, 8x4 bits, N = 4096: 12.1 us here against
-  // 15.5; N = 16384: 23.5 against 17.2.
-  if (a.T > 128 && mx_ceil(a.T, 128) * mx_ceil(a.N, kLM) > a.num_sms) return launch_mx_gemm(a, st);
   const LinPlan p = plan_linear(a.T, a.N, a.K, XF == STRATA_MX_FP4 && WF == STRATA_MX_FP4, a.num_sms);
-  if (p.nt == 16) return launch_linear<XF, WF, 16>(a, p.splits, st);
-  if (p.nt == 32) return launch_linear<XF, WF, 32>(a, p.splits, st);
-  if (p.nt == 64) return launch_linear<XF, WF, 64>(a, p.splits, st);
-  return launch_linear<XF, WF, 128>(a, p.splits, st);
+  switch (p.nt) {
+    case 0: return launch_mx_gemm(a, st);
+    case 16: return launch_linear<XF, WF, 16>(a, p.splits, st);
+    case 32: return launch_linear<XF, WF, 32>(a, p.splits, st);
+    case 64: return launch_linear<XF, WF, 64>(a, p.splits, st);
+    default: return launch_linear<XF, WF, 128>(a, p.splits, st);
+  }
 }
 
 }  // namespace

@@ -378,6 +378,20 @@ def test_linear_same_bits_every_time_and_in_any_batch_of_a_tile():
         assert torch.equal(a, sm.mx_linear(x, w, out_dtype=torch.float32))
 
 
+@pytest.mark.parametrize("T", [1 << 22, (1 << 20) + 1])
+def test_linear_most_tokens(T):
+    """Small integers, exact in any order; N too small for many tiles."""
+    g = gen(70)
+    x = torch.randint(-3, 4, (1024, 128), device=DEV, generator=g).float()
+    w = torch.randint(-3, 4, (3, 128), device=DEV, generator=g).float()
+    q = sm.mx_quantize(x, sm.MX_FP8, sm.MX_ROWS)
+    n = -(-T // 1024)
+    many = sm.mx_tile_scales(sm.MXTensor(q.codes.repeat(n, 1)[:T], q.scales.repeat(n, 1)[:T], sm.MX_FP8, T, 128,
+                                         sm.MX_ROWS))
+    y = sm.mx_linear(many, sm.mx_quantize(w, sm.MX_FP4), out_dtype=torch.float32)
+    assert torch.equal(y, (x @ w.T).repeat(n, 1)[:T])
+
+
 def test_linear_nothing():
     w, _ = random_mx(64, 128, sm.MX_FP4, 12)
     x = sm.mx_quantize(torch.empty(0, 128, device=DEV), sm.MX_FP8)
