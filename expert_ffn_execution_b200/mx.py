@@ -39,7 +39,8 @@ def _library():
     global _fast
     lib = B._lib or B.load()
     if _fast is None and _mxcalls is not None:
-        names = ("moe_mx_quantize", "moe_mx_dequantize", "moe_add_rmsnorm", "moe_mx_linear")
+        names = ("moe_mx_quantize", "moe_mx_dequantize", "moe_add_rmsnorm", "moe_mx_linear",
+                 "moe_mx_pack_experts", "moe_mx_unpack_experts", "strata_expert_bytes")
         _mxcalls.setup(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
                        torch.Tensor, torch.nn.Parameter, MXTensor, AddNorm)
         _fast = _mxcalls
@@ -319,6 +320,8 @@ def pack_experts(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
                  stream=None) -> ExpertWeights:
     """Quantises E experts' weights, gate and up [E, I, H], down [E, H, I], all
     of one dtype, to the MXFP4 blobs that moe_experts reads."""
+    if _fast and (blobs := _fast.pack(gate, up, down, stream)) is not None:
+        return ExpertWeights(blobs, B.FMT_MXFP4_32, gate.shape[2], gate.shape[1])
     if gate.dim() != 3 or up.shape != gate.shape:
         raise ValueError("gate and up must be [E, I, H]")
     E, I, H = gate.shape
@@ -349,6 +352,8 @@ def unpack_experts(w: ExpertWeights, dtype=torch.float32, stream=None):
     """(gate, up, down) that MXFP4 blobs stand for: [E, I, H] twice, [E, H, I]."""
     if w.fmt != B.FMT_MXFP4_32:
         raise ValueError("only MXFP4 blobs are read back")
+    if _fast and (made := _fast.unpack(w.blobs, w.hidden, w.inter, dtype, stream)) is not None:
+        return made
     dt, dev, E, H, I = _dtype(dtype), _device(w.blobs), w.num_experts, w.hidden, w.inter
     if _elsewhere(dev):
         with torch.cuda.device(dev):

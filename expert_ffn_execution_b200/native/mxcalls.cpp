@@ -39,6 +39,9 @@ struct Library {
   decltype(&moe_mx_dequantize) dequantize;
   decltype(&moe_add_rmsnorm) add_rmsnorm;
   decltype(&moe_mx_linear) linear;
+  decltype(&moe_mx_pack_experts) pack;
+  decltype(&moe_mx_unpack_experts) unpack;
+  decltype(&strata_expert_bytes) expert_bytes;
 } lib;
 PyObject* torch_tensor;    // torch.Tensor
 PyObject* torch_param;     // torch.nn.Parameter
@@ -151,14 +154,14 @@ struct Tensor {
   int index = -1;
   void* ptr = nullptr;
   int dims = 0;
-  int64_t size[2] = {0, 0}, stride[2] = {0, 0};
+  int64_t size[3] = {0, 0, 0}, stride[3] = {0, 0, 0};
   bool rows_contiguous() const {
     return dims == 2 && (size[1] <= 1 || stride[1] == 1) &&
            (size[0] <= 1 || stride[0] == size[1] || size[1] == 0);
   }
 };
 
-// Reads a torch.Tensor (or Parameter; no other subclass) of one or two
+// Reads a torch.Tensor (or Parameter; no other subclass) of one to three
 // dimensions on a CUDA device.  Throws for one without memory of its own.
 bool read(PyObject* o, Tensor* t) {
   PyObject* type = reinterpret_cast<PyObject*>(Py_TYPE(o));
@@ -169,7 +172,7 @@ bool read(PyObject* o, Tensor* t) {
   t->dtype = st == at::kByte ? 8 : st == at::kInt ? 32 : dtype_of(st);
   t->index = v.device().index();
   t->dims = (int)v.dim();
-  if (t->dtype < 0 || t->index < 0 || t->index >= 64 || (t->dims != 1 && t->dims != 2)) return false;
+  if (t->dtype < 0 || t->index < 0 || t->index >= 64 || t->dims < 1 || t->dims > 3) return false;
   const at::IntArrayRef size = v.sizes(), stride = v.strides();
   for (int i = 0; i < t->dims; ++i) {
     t->size[i] = size[i];
@@ -460,11 +463,72 @@ PyObject* linear(PyObject* const* args, Py_ssize_t n) {
   return has_out ? Py_NewRef(args[4]) : THPVariable_Wrap(std::move(y));
 }
 
+PyObject* pack(PyObject* const* args, Py_ssize_t n) {  // gate, up, down, stream: the blobs
+  Tensor w[3];
+  void* stream;
+  if (n != 4) NOT_TAKEN;
+  int64_t rows[3], experts[3];
+  for (int i = 0; i < 3; ++i) {
+    if (!read(args[i], &w[i]) || w[i].dims != 3 || w[i].dtype > 2 || w[i].stride[2] != 1 ||
+        w[i].dtype != w[0].dtype || w[i].index != w[0].index)
+      NOT_TAKEN;
+    rows[i] = w[i].stride[1];
+    experts[i] = w[i].stride[0];
+  }
+  const int64_t E = w[0].size[0], I = w[0].size[1], H = w[0].size[2];
+  if (E < 1 || I < 128 || H < 128 || E >> 31 || I >> 31 || H >> 31 || w[1].size[0] != E ||
+      w[1].size[1] != I || w[1].size[2] != H || w[2].size[0] != E || w[2].size[1] != H ||
+      w[2].size[2] != I || !target(w[0].index, args[3], &stream))
+    NOT_TAKEN;
+  at::Tensor blobs;
+  const int32_t rc = launch([&] {
+    const int64_t bytes = (int64_t)lib.expert_bytes(STRATA_FMT_MXFP4_32, (int32_t)H, (int32_t)I);
+    if (!bytes) return (int32_t)STRATA_EINVAL;
+    blobs = empty({E, bytes}, at::kByte, w[0].index);
+    return lib.pack(w[0].ptr, w[1].ptr, w[2].ptr, w[0].dtype, rows, experts, (int32_t)E, (int32_t)H,
+                    (int32_t)I, blobs.data_ptr(), (uint64_t)bytes, stream);
+  });
+  if (rc != STRATA_OK) NOT_TAKEN;
+  return THPVariable_Wrap(std::move(blobs));
+}
+
+PyObject* unpack(PyObject* const* args, Py_ssize_t n) {  // blobs, H, I, dtype, stream
+  Tensor b;
+  long H, I;
+  void* stream;
+  if (n != 5 || !read(args[0], &b) || b.dims != 2 || b.dtype != 8 || b.stride[1] != 1 ||
+      b.size[0] >> 31 || !small_int(args[1], &H) || !small_int(args[2], &I) || H < 128 || I < 128 ||
+      H >> 31 || I >> 31)
+    NOT_TAKEN;
+  const int dt = dtype_of(args[3]);
+  if (dt < 0 || !target(b.index, args[4], &stream)) NOT_TAKEN;
+  at::Tensor w[3];
+  const int32_t rc = launch([&] {
+    for (int i = 0; i < 3; ++i)
+      w[i] = i < 2 ? empty({b.size[0], I, H}, scalar_type(dt), b.index)
+                   : empty({b.size[0], H, I}, scalar_type(dt), b.index);
+    return lib.unpack(b.ptr, (uint64_t)b.stride[0], (int32_t)b.size[0], (int32_t)H, (int32_t)I,
+                      w[0].data_ptr(), w[1].data_ptr(), w[2].data_ptr(), dt, stream);
+  });
+  if (rc != STRATA_OK) NOT_TAKEN;
+  PyObject* all = PyTuple_New(3);
+  for (int i = 0; all && i < 3; ++i) {
+    PyObject* o = THPVariable_Wrap(std::move(w[i]));
+    if (!o) {
+      Py_CLEAR(all);
+      break;
+    }
+    PyTuple_SET_ITEM(all, i, o);
+  }
+  return all;
+}
+
 // setup(addresses, torch.Tensor, Parameter, MXTensor, AddNorm)
 PyObject* setup(PyObject*, PyObject* args) {
-  unsigned long long f[4];
+  unsigned long long f[7];
   PyObject* o[4];
-  if (!PyArg_ParseTuple(args, "(KKKK)OOOO", &f[0], &f[1], &f[2], &f[3], &o[0], &o[1], &o[2], &o[3]))
+  if (!PyArg_ParseTuple(args, "(KKKKKKK)OOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &o[0],
+                        &o[1], &o[2], &o[3]))
     return nullptr;
   if (!PyType_Check(o[2]) || !PyType_IsSubtype((PyTypeObject*)o[2], matrix_type) ||
       !PyType_Check(o[3]) || !PyType_IsSubtype((PyTypeObject*)o[3], &PyTuple_Type)) {
@@ -475,6 +539,9 @@ PyObject* setup(PyObject*, PyObject* args) {
   lib.dequantize = reinterpret_cast<decltype(lib.dequantize)>(f[1]);
   lib.add_rmsnorm = reinterpret_cast<decltype(lib.add_rmsnorm)>(f[2]);
   lib.linear = reinterpret_cast<decltype(lib.linear)>(f[3]);
+  lib.pack = reinterpret_cast<decltype(lib.pack)>(f[4]);
+  lib.unpack = reinterpret_cast<decltype(lib.unpack)>(f[5]);
+  lib.expert_bytes = reinterpret_cast<decltype(lib.expert_bytes)>(f[6]);
   Py_XSETREF(torch_tensor, Py_NewRef(o[0]));
   Py_XSETREF(torch_param, Py_NewRef(o[1]));
   Py_XSETREF(mx_type, reinterpret_cast<PyTypeObject*>(Py_NewRef(o[2])));
@@ -490,6 +557,8 @@ PyMethodDef methods[] = {
     CALL(dequantize),
     CALL(add_rmsnorm),
     CALL(linear),
+    CALL(pack),         // pack_experts' blobs, or None
+    CALL(unpack),       // what unpack_experts returns, or None
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_mxcalls",

@@ -759,3 +759,39 @@ def test_native_calls_of_several_threads():
     for i, got in enumerate(gots):
         for once in got:
             assert all(torch.equal(a, b) for a, b in zip(once, want[i]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_native_expert_calls_are_the_python_ones(monkeypatch, dtype):
+    g = gen(82)
+    ws = [torch.randn(3, *s, device=DEV, generator=g).to(dtype) for s in ((128, 384), (128, 384), (384, 128))]
+    made = []
+    for fast in (mx._fast, None):
+        monkeypatch.setattr(mx, "_fast", fast)
+        if fast is None:
+            monkeypatch.setattr(mx, "_mxcalls", None)
+        e = sm.pack_experts(*ws)
+        made.append((e, e.dequantize(), e.dequantize(torch.float16)))
+    (a, *x), (b, *y) = made
+    assert (a.fmt, a.hidden, a.inter, a.num_experts, a.blobs.shape, a.qw.expert_stride) == \
+        (b.fmt, b.hidden, b.inter, b.num_experts, b.blobs.shape, b.qw.expert_stride) and a.hidden == 384
+    for p, q in zip(x, y):
+        for u, v in zip(p, q):
+            assert u.dtype == v.dtype and u.shape == v.shape and torch.equal(u, v)
+
+
+def test_native_expert_calls_leave_refusals_to_python():
+    w = torch.zeros(2, 128, 256, device=DEV)
+    d = torch.zeros(2, 256, 128, device=DEV)
+    e = sm.pack_experts(w, w, d)
+    for call, error, match in (
+            (lambda: sm.pack_experts(w[0], w, d), ValueError, "gate and up"),
+            (lambda: sm.pack_experts(w, w, w), ValueError, "down"),
+            (lambda: sm.pack_experts(w[:, :96], w[:, :96], d[:, :, :96]), ValueError, "128"),
+            (lambda: sm.pack_experts(w[:0], w[:0], d[:0]), ValueError, "positive"),
+            (lambda: sm.pack_experts(w, w.half(), d), TypeError, "one dtype"),
+            (lambda: sm.pack_experts(w, w, d.transpose(1, 2).contiguous().transpose(1, 2)), ValueError, "rows"),
+            (lambda: sm.pack_experts(w.cpu(), w, d), ValueError, "CUDA"),
+            (lambda: e.dequantize(torch.int32), TypeError, "dtype")):
+        with pytest.raises(error, match=match):
+            call()
