@@ -162,7 +162,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* issued = reinterpret_cast<int*>(tmem_slot + 2);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // the warp from one lane: known to be the same in all, as is what follows from it
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   const int chunks = (a.K + C::KS - 1) / C::KS;
@@ -187,36 +188,32 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   __syncthreads();
   cluster_sync_relaxed();  // both CTAs' barriers and tensor memory are ready
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait_prior();
 
   if (warp == kGEpi) {
     // ------------------------------------------------ copies, counted on the even CTA's barriers
-    if (elect_one()) {
-      int i = 0;
-      bool ok = true;
-      for (int tile = pair; tile < tiles && ok; tile += pairs) {
-        const int t0 = (tile % mt) * kGM, n0 = (tile / mt) * kGN;
-        for (int ch = 0; ch < chunks; ++ch, ++i) {
-          const int s = i % C::S;
-          if (!mbar_wait_guarded(&empty[s], ((i / C::S) & 1) ^ 1, a.status, abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0)
-            mbar_arrive_expect_tx(&full[s], 2u * (C::AB + C::BTx + C::SA + C::SBb));
-          uint8_t* st = smem + s * C::stride;
-          const uint32_t bar = cluster_addr(smem_addr(&full[s]), 0);
-          const int kx = (int)mx_row_bytes(XF, (int64_t)ch * C::KS);
-          const int kw = C::kSpread ? ch * C::KS : (int)mx_row_bytes(WF, (int64_t)ch * C::KS);
-          tma_load_2d_pair(st, &xmap, kx, t0 + 128 * (int)rank, bar);
-          tma_load_2d_pair(st + C::AB, &wmap, kw, n0 + 128 * (int)rank, bar);
-          tma_load_2d_pair(st + C::AB + C::BB, &xsmap, ch * C::ST * 64, t0 / 128 + (int)rank, bar);
-          tma_load_2d_pair(st + C::AB + C::BB + C::SA, &wsmap, ch * C::ST * 64, n0 / 128, bar);
-        }
+    int i = 0, s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      const int t0 = (tile % mt) * kGM, n0 = (tile / mt) * kGN;
+      for (int ch = 0; ch < chunks; ++ch, ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait_guarded(&empty[s], ph, a.status, abort_flag));
+        if (!ok) break;
+        uint8_t* st = smem + s * C::stride;
+        const int kx = (int)mx_row_bytes(XF, (int64_t)ch * C::KS);
+        const int kw = C::kSpread ? ch * C::KS : (int)mx_row_bytes(WF, (int64_t)ch * C::KS);
+        load_stage_pair_warp(
+            rank == 0 ? &full[s] : nullptr, 2u * (C::AB + C::BTx + C::SA + C::SBb),
+            cluster_addr(smem_addr(&full[s]), 0), {&xmap, kx, t0 + 128 * (int)rank, st},
+            {&wmap, kw, n0 + 128 * (int)rank, st + C::AB},
+            {&xsmap, ch * C::ST * 64, t0 / 128 + (int)rank, st + C::AB + C::BB},
+            {&wsmap, ch * C::ST * 64, n0 / 128, st + C::AB + C::BB + C::SA});
+        if (++s == C::S) s = 0, ph ^= 1u;
       }
-      *issued = i;
     }
+    *issued = i;
     __syncwarp();
   } else if (warp == kGEpi + 1) {
     // ------------------------------------------------ MMAs, by the even CTA for both
@@ -225,39 +222,33 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       const uint32_t smem0 = smem_addr(smem);
       constexpr uint32_t xf = C::F4 ? 1u : XF == STRATA_MX_FP4 ? 5u : 0u;
       constexpr uint32_t wf = C::F4 ? 1u : WF == STRATA_MX_FP4 ? 5u : 0u;
-      int i = 0, it = 0;
+      int s = 0, it = 0;
+      uint32_t ph = 0;
       bool ok = true;
       for (int tile = pair; tile < tiles && ok; tile += pairs, ++it) {
         ok = mbar_wait_guarded(tempty, (it & 1) ^ 1, a.status, abort_flag);
         tc_fence_after();
-        for (int ch = 0; ch < chunks && ok; ++ch, ++i) {
-          const int s = i % C::S;
-          ok = mbar_wait_guarded(&full[s], (i / C::S) & 1, a.status, abort_flag);
+        for (int ch = 0; ch < chunks && ok; ++ch) {
+          ok = mbar_wait_guarded(&full[s], ph, a.status, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const int left = a.K - ch * C::KS;  // a multiple of 128
           const uint32_t st = smem0 + (uint32_t)(s * C::stride);
           const uint32_t ssa = st + C::AB + C::BB, ssb = ssa + C::SA;
           const uint32_t sfx = tbase + kGN + s * C::sfcols, sfw = sfx + 4 * C::ST;
-#pragma unroll
-          for (int b = 0; b < C::ST; ++b) {
-            tmem_cp_scales_pair(sfx + 4 * b, smem_desc_scale_lo(ssa + b * kMxTileBytes));
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              tmem_cp_scales_pair(sfw + 8 * b + 4 * r,
-                                  smem_desc_scale_lo(ssb + (r * C::ST + b) * kMxTileBytes));
-          }
           const uint32_t xlo = smem_desc_k128_lo(st), wlo = smem_desc_k128_lo(st + C::AB);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j * C::KI < left) {
-              const int b = C::F4 ? j / 2 : 0;
-              const uint32_t sf = C::F4 ? 2u * (j & 1) : (uint32_t)j;
-              mma_mx_pair<C::F4>(tbase, xlo + 2 * j, wlo + 2 * j, hi, idesc_mx(xf, wf, kGM, kGN, sf),
-                                 sfx + 4 * b, sfw + 8 * b, (uint32_t)(ch + j > 0));
+          for (int b = 0; b < C::ST; ++b) {
+            if (b * 128 < left) {
+              const uint32_t sw = ssb + b * kMxTileBytes;  // of the first 128 features
+              mma_mx_block<C::F4, true>(
+                  tbase, xlo + 4 * b, wlo + 4 * b, hi, idesc_mx(xf, wf, kGM, kGN, 0), sfx + 4 * b,
+                  sfw + 8 * b, sfw + 8 * b, smem_desc_scale_lo(ssa + b * kMxTileBytes),
+                  smem_desc_scale_lo(sw), smem_desc_scale_lo(sw + C::SA), (uint32_t)(ch + b > 0));
             }
           }
           mma_commit_pair(&empty[s]);
+          if (++s == C::S) s = 0, ph ^= 1u;
         }
         if (ok) mma_commit_pair(tfull);
       }

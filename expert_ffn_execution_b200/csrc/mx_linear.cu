@@ -148,7 +148,8 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* issued = reinterpret_cast<int*>(tmem_slot + 2);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // the warp from one lane: known to be the same in all, as is what follows from it
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   // (shifts: divisions here took 0.3 us before the first barrier)
   const int splits = 1 << lg_splits;
   const int rank = splits > 1 ? (int)cluster_ctarank() : 0;
@@ -180,7 +181,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   if (splits > 1) {
     if (threadIdx.x == 0)  // every rank sends this one its sums of `mine` tokens
       mbar_arrive_expect_tx(joined, (uint32_t)(mine * splits * C::token));
@@ -190,71 +191,56 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
   pdl_wait_prior();
 
   if (warp == 4) {
-    if (elect_one()) {
-      int i = 0, s = 0;
-      uint32_t ph = 1;
-      for (; i < nch; ++i) {
-        if (!mbar_wait_guarded(&empty[s], ph, a.status, abort_flag)) break;
-        const int ch = c0 + i;
-        const int nst = min(C::ST, kt - ch * C::ST);  // scale tiles left along K
-        uint8_t* st = smem + s * C::stride;
-        mbar_arrive_expect_tx(&full[s], C::WTx + C::XB + 2u * nst * kMxTileBytes);
-        // coordinates in the map's elements: codes of the spread type, else bytes
-        const int kw = C::kSpread ? ch * C::KS : (int)mx_row_bytes(WF, (int64_t)ch * C::KS);
-        const int kx = (int)mx_row_bytes(XF, (int64_t)ch * C::KS);
-        tma_load_2d(st, &wmap, kw, n0, &full[s]);
-        tma_load_2d(st + C::WB, &xmap, kx, t0, &full[s]);
-        bulk_g2s(st + C::WB + C::XB,
-                 a.w_scales + ((int64_t)(n0 / 128) * kt + ch * C::ST) * kMxTileBytes,
-                 (uint32_t)nst * kMxTileBytes, &full[s]);
-        bulk_g2s(st + C::WB + C::XB + C::SB,
-                 a.x_scales + ((int64_t)(t0 / 128) * kt + ch * C::ST) * kMxTileBytes,
-                 (uint32_t)nst * kMxTileBytes, &full[s]);
-        if (++s == S) s = 0, ph ^= 1u;
-      }
-      *issued = i;
+    int i = 0, s = 0;
+    uint32_t ph = 1;
+    for (; i < nch; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait_guarded(&empty[s], ph, a.status, abort_flag))) break;
+      const int ch = c0 + i;
+      const uint32_t scales = (uint32_t)min(C::ST, kt - ch * C::ST) * kMxTileBytes;  // left along K
+      uint8_t* st = smem + s * C::stride;
+      // coordinates in the map's elements: codes of the spread type, else bytes
+      const int kw = C::kSpread ? ch * C::KS : (int)mx_row_bytes(WF, (int64_t)ch * C::KS);
+      const int kx = (int)mx_row_bytes(XF, (int64_t)ch * C::KS);
+      load_stage_warp(&full[s], C::WTx + C::XB + 2 * scales, &wmap, kw, n0, st, &xmap, kx, t0,
+                      st + C::WB,
+                      a.w_scales + ((int64_t)(n0 / 128) * kt + ch * C::ST) * kMxTileBytes,
+                      st + C::WB + C::XB,
+                      a.x_scales + ((int64_t)(t0 / 128) * kt + ch * C::ST) * kMxTileBytes,
+                      st + C::WB + C::XB + C::SB, scales);
+      if (++s == S) s = 0, ph ^= 1u;
     }
+    *issued = i;
     __syncwarp();
   } else if (warp == 5) {
-    if (elect_one()) {
-      const uint32_t hi = smem_desc_k128_hi(1024);
-      const uint32_t stages = smem_addr(smem);
-      constexpr uint32_t wf = C::F4 ? 1u : WF == STRATA_MX_FP4 ? 5u : 0u;
-      constexpr uint32_t xf = C::F4 ? 1u : XF == STRATA_MX_FP4 ? 5u : 0u;
-      int s = 0;
-      uint32_t ph = 0;
-      for (int i = 0; i < nch; ++i) {
-        if (!mbar_wait_guarded(&full[s], ph, a.status, abort_flag)) break;
-        tc_fence_after();
-        const int left = a.K - (c0 + i) * C::KS;  // a multiple of 128
-        const uint32_t st = stages + (uint32_t)(s * C::stride);
-        // a tile that starts 64 tokens into its scale tile reads two columns on
-        const uint32_t sfw = tbase + C::dcols + s * C::sfcols, sfx = sfw + 4 * C::ST;
-        const uint32_t sfx_at = sfx + (NT == 64 ? (t0 % 128) / 32 : 0);
+    const uint32_t hi = smem_desc_k128_hi(1024);
+    const uint32_t stages = smem_addr(smem);
+    constexpr uint32_t wf = C::F4 ? 1u : WF == STRATA_MX_FP4 ? 5u : 0u;
+    constexpr uint32_t xf = C::F4 ? 1u : XF == STRATA_MX_FP4 ? 5u : 0u;
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < nch; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait_guarded(&full[s], ph, a.status, abort_flag))) break;
+      tc_fence_after();
+      const int left = a.K - (c0 + i) * C::KS;  // a multiple of 128
+      const uint32_t st = stages + (uint32_t)(s * C::stride);
+      // a tile that starts 64 tokens into its scale tile reads two columns on
+      const uint32_t sfw = tbase + C::dcols + s * C::sfcols, sfx = sfw + 4 * C::ST;
+      const uint32_t sfx_at = sfx + (NT == 64 ? (t0 % 128) / 32 : 0);
+      const uint32_t wlo = smem_desc_k128_lo(st), xlo = smem_desc_k128_lo(st + C::WB);
 #pragma unroll
-        for (int b = 0; b < C::ST; ++b) {
-          if (b * 128 < left) {
-            tmem_cp_scales(sfw + 4 * b, smem_desc_scale_lo(st + C::WB + C::XB + b * kMxTileBytes));
-            tmem_cp_scales(sfx + 4 * b,
-                           smem_desc_scale_lo(st + C::WB + C::XB + C::SB + b * kMxTileBytes));
-          }
+      for (int b = 0; b < C::ST; ++b) {
+        if (b * 128 < left) {
+          const uint32_t scales = st + C::WB + C::XB + b * kMxTileBytes;
+          mma_mx_block<C::F4, false>(
+              tbase, wlo + 4 * b, xlo + 4 * b, hi, idesc_mx(wf, xf, kLM, NT, 0), sfw + 4 * b,
+              sfx + 4 * b, sfx_at + 4 * b, smem_desc_scale_lo(scales),
+              smem_desc_scale_lo(scales + C::SB), 0u, (uint32_t)(i + b > 0));
         }
-        const uint32_t wlo = smem_desc_k128_lo(st), xlo = smem_desc_k128_lo(st + C::WB);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j * C::KI < left) {
-            // two instructions share a scale column at K = 64, four at K = 32
-            const int b = C::F4 ? j / 2 : 0;
-            const uint32_t sf = C::F4 ? 2u * (j & 1) : (uint32_t)j;
-            mma_mx<C::F4>(tbase, wlo + 2 * j, xlo + 2 * j, hi, idesc_mx(wf, xf, kLM, NT, sf),
-                          sfw + 4 * b, sfx_at + 4 * b, (uint32_t)(i + j > 0));
-          }
-        }
-        mma_commit(&empty[s]);
-        if (++s == S) s = 0, ph ^= 1u;
       }
-      mma_commit(tfull);
+      mma_commit_warp(&empty[s]);
+      if (++s == S) s = 0, ph ^= 1u;
     }
+    mma_commit_warp(tfull);
     __syncwarp();
   } else {
     const bool ok = __all_sync(0xffffffffu, mbar_wait_guarded(tfull, 0, a.status, abort_flag) &&

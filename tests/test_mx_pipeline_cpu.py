@@ -224,8 +224,9 @@ def test_the_model_is_of_the_kernels():
     """The counts and parities that the model has are the kernels'."""
     gemm = open(os.path.join(CSRC, "mx_gemm.cu")).read()
     for line in ("mbar_init(&full[s], 1);", "mbar_init(&empty[s], 1);", "mbar_init(tfull, 1);",
-                 "mbar_init(tempty, 2 * kGEpi);", "mbar_wait_guarded(&empty[s], ((i / C::S) & 1) ^ 1",
-                 "mbar_wait_guarded(&full[s], (i / C::S) & 1", "mbar_wait_guarded(tempty, (it & 1) ^ 1",
+                 "mbar_init(tempty, 2 * kGEpi);", "mbar_wait_guarded(&empty[s], ph,",
+                 "mbar_wait_guarded(&full[s], ph,", "uint32_t ph = 1;", "uint32_t ph = 0;",
+                 "if (++s == C::S) s = 0, ph ^= 1u;", "mbar_wait_guarded(tempty, (it & 1) ^ 1",
                  "mbar_wait_guarded(tfull, it & 1", "mma_commit_pair(&empty[s]);", "mma_commit_pair(tfull);"):
         assert line in gemm, line
     linear = open(os.path.join(CSRC, "mx_linear.cu")).read()
