@@ -16,7 +16,7 @@
 // in rank order.  Joining is a matter of round trips: with T = 4, N = 2560, K =
 // 2560, 8x4 bits, fetching the sums 16 bytes at a time behind a barrier that
 // orders memory took 5.2 us, and 4.5 us once each CTA sent a rank its tokens
-// by one bulk copy that counts on the receiver's barrier (4.0 us now).
+// by one bulk copy that counts on the receiver's barrier (3.9 us now).
 #include <algorithm>
 #include <cmath>
 
@@ -357,17 +357,17 @@ cudaError_t launch_linear(const MxLinearArgs& a, int splits, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, wmap, xmap, a, lg, S);
 }
 
-// The form of a call, by what it costs in units of the 0.2 us that a stage of
-// 128 weight rows and 16 token rows takes its SM (2.5 cycles a 128-byte row,
-// whichever CTA it belongs to; the 8-bit operands' instructions hide behind
-// that, four bits' half as many stages take 1.9).  The factors are fitted to
-// every form's time on 788 shapes (1 to 1100 tokens, N to 24000, K to 8192,
-// all three pairs of formats): this takes the best form or one within 8 % of
-// it for 779, on average within 0.4 %.  Measured, T = 4, 8x4 bits, with 1, 2,
-// 4 and 8 ranks: N = 2560, K = 8192 15.9, 10.1, 7.5 and 6.7 us; N = 8192, K =
-// 2048 6.5, 5.9 and 5.5 with 1, 2 and 4.  T = 256, K = 4096, N = 4096: 11.9 us
-// in tiles of 64 tokens, 15.5 in the pairs' tiles; N = 16384: 23.5 in tiles of
-// 128, 17.2 in the pairs'.
+// The form of a call, by what it costs: the stages that a CTA goes through
+// (0.16 to 0.22 us each, most of it the issue of the scale copies and MMAs,
+// so the tile's tokens count for little), CTAs an SM, the join, reading the
+// sums out.  The factors, in units of 0.2 us, are fitted to every form's time
+// on 788 shapes (1 to 1100 tokens, N to 24000, K to 8192, all three pairs of
+// formats).  On 1262 others this takes the best form or one within 8 % of it
+// for 1229, and is 0.5 % behind on average.  Measured, T = 4, 8x4 bits, with
+// 1, 2, 4 and 8 ranks: N = 2560, K = 8192 15.9, 10.1, 7.5 and 6.7 us; N = 8192,
+// K = 2048 6.5, 5.9 and 5.5 with 1, 2 and 4.  T = 256, K = 4096, N = 4096: 11.9
+// us in tiles of 64 tokens, 15.5 in the pairs' tiles; N = 16384: 23.5 in tiles
+// of 128, 17.2 in the pairs'.
 struct LinPlan {
   int nt, splits;  // tokens a tile, 0: the pairs' tiles; ranks a tile
 };
