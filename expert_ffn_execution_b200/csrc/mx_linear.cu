@@ -74,61 +74,55 @@ STRATA_DEVFN void store1(void* y, int64_t i, float v) {
   else
     reinterpret_cast<uint16_t*>(y)[i] = (uint16_t)pack2<DT>(v, v);
 }
-template <int DT>
-STRATA_DEVFN void store4(void* y, int64_t i, const float (&v)[4]) {
-  if constexpr (DT == STRATA_DTYPE_F32)
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(y) + i) =
-        make_float4(v[0], v[1], v[2], v[3]);
+template <int N>  // N columns of this warp's 32 lanes
+STRATA_DEVFN void tmem_load(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 16 || N == 32, "what a tile has");
+  if constexpr (N == 16)
+    tmem_ld16(taddr, r);
   else
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(y) + i) =
-        make_uint2(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]));
+    tmem_ld32(taddr, r);
+  tmem_wait_ld();
 }
-
-// Sums [rank][token][feature], ranks `per` tokens apart, of `count` tokens from
-// t0 on -> y, rank by rank.  A lane has four features of a token: adjacent
-// ones, stored together, where all rows of the tile are aligned for that and
-// inside y, else ones 32 apart, so that the lanes' stores are side by side.
-template <int DT>
-STRATA_DEVFN void write_y(const MxLinearArgs& a, const uint8_t* sums, int n0, int t0, int count,
-                          int per, int splits) {
-  constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
-  const int rank_floats = per * kLM, left = a.N - n0;
-  const bool vec = left >= kLM && a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * kEl) == 0;
-  const int lane = threadIdx.x % 32, f0 = vec ? 4 * lane : lane, df = vec ? 1 : 32;
-  float bias[4] = {0.f, 0.f, 0.f, 0.f};
-  if (a.bias) {
+// The sums of this warp's 32 features and `count` tokens in tensor memory -> y,
+// element i on for the lane's feature (`some`: it is one of y's).  A lane has a
+// feature and its tokens are registers, so a token's store is 32 elements side
+// by side, on any alignment, and takes few instructions: through shared memory
+// and by wider stores 64 tokens took 4900 cycles after the last MMA, of code
+// that runs once.
+template <int DT, int NT>
+STRATA_DEVFN void write_sums(const MxLinearArgs& a, uint32_t taddr, int64_t i, bool some,
+                             float bias, int count) {
+  constexpr int kLoad = NT < 32 ? 16 : 32;
+#pragma unroll 1
+  for (int c = 0; c < count; c += kLoad) {
+    uint32_t r[kLoad];
+    tmem_load<kLoad>(taddr + c, r);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (f0 + k * df < left) bias[k] = a.bias[n0 + f0 + k * df];
+    for (int k = 0; k < kLoad; ++k, i += a.ldy)
+      if (some && c + k < count) store1<DT>(a.y, i, __uint_as_float(r[k]) + bias);
   }
+}
+// Sums [rank][token][feature], ranks `per` tokens apart, of `count` tokens, rank
+// by rank -> y, element i on for this thread's feature.
+template <int DT, int SPLITS>
+STRATA_DEVFN void write_joined(const MxLinearArgs& a, const float* sums, int64_t i, float bias,
+                               int count, int per) {
 #pragma unroll 2
-  for (int t = threadIdx.x / 32; t < count; t += kLThreads / 32) {
-    const float* at = reinterpret_cast<const float*>(sums) + t * kLM + f0;
-    const int64_t o = (int64_t)(t0 + t) * a.ldy + n0 + f0;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (vec) {
-      for (int q = 0; q < splits; ++q) {
-        const float4 u = *reinterpret_cast<const float4*>(at + q * rank_floats);
-        v[0] += u.x;
-        v[1] += u.y;
-        v[2] += u.z;
-        v[3] += u.w;
-      }
-    } else {
-      for (int q = 0; q < splits; ++q)
+  for (int t = 0; t < count; ++t, i += a.ldy, sums += kLM) {
+    float v[SPLITS];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] += at[q * rank_floats + 32 * k];
-    }
+    for (int q = 0; q < SPLITS; ++q) v[q] = sums[q * per * kLM];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] += bias[k];
-    if (vec) {
-      store4<DT>(a.y, o, v);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (f0 + 32 * k < left) store1<DT>(a.y, o + 32 * k, v[k]);
-    }
+    for (int q = 1; q < SPLITS; ++q) v[0] += v[q];
+    store1<DT>(a.y, i, v[0] + bias);
   }
+}
+template <int DT>
+STRATA_DEVFN void write_joined(const MxLinearArgs& a, const float* sums, int64_t i, float bias,
+                               int count, int per, int splits) {
+  if (splits == 2) write_joined<DT, 2>(a, sums, i, bias, count, per);
+  if (splits == 4) write_joined<DT, 4>(a, sums, i, bias, count, per);
+  if (splits == 8) write_joined<DT, 8>(a, sums, i, bias, count, per);
 }
 
 template <int XF, int WF, int NT>
@@ -188,6 +182,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     __syncwarp();
     cluster_arrive_relaxed();  // waited for before the first copy to another rank
   }
+  const int n = n0 + (int)threadIdx.x;  // the feature of a thread that reads sums
+  const bool some = (int)threadIdx.x < kLM && n < a.N;
+  float bias = 0.f;
   pdl_wait_prior();
 
   if (warp == 4) {
@@ -243,20 +240,29 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     mma_commit_warp(tfull);
     __syncwarp();
   } else {
+    if (some && a.bias) bias = a.bias[n];
     const bool ok = __all_sync(0xffffffffu, mbar_wait_guarded(tfull, 0, a.status, abort_flag) &&
                                                 !*abort_flag);
     tc_fence_after();
-    // sums -> shared memory [token][feature], over the stages
-    float* red = reinterpret_cast<float*>(smem);
-    const int f = warp * 32 + lane;
-    if (ok) {
+    const uint32_t tq = tbase + ((uint32_t)(warp * 32) << 16);
+    if (ok && splits == 1) {
+      const int64_t y0 = (int64_t)t0 * a.ldy + n;
+      if (a.y_dtype == STRATA_DTYPE_F32)
+        write_sums<STRATA_DTYPE_F32, NT>(a, tq, y0, some, bias, nt);
+      else if (a.y_dtype == STRATA_DTYPE_F16)
+        write_sums<STRATA_DTYPE_F16, NT>(a, tq, y0, some, bias, nt);
+      else
+        write_sums<STRATA_DTYPE_BF16, NT>(a, tq, y0, some, bias, nt);
+    } else if (ok) {
+      // sums -> shared memory [token][feature], over the stages
+      constexpr int kLoad = NT < 32 ? 16 : 32;
+      float* red = reinterpret_cast<float*>(smem) + threadIdx.x;
 #pragma unroll 1
-      for (int c = 0; c < NT && t0 + c < a.T; c += 16) {
-        uint32_t r[16];
-        tmem_ld16(tbase + ((uint32_t)(warp * 32) << 16) + c, r);
-        tmem_wait_ld();
+      for (int c = 0; c < nt; c += kLoad) {
+        uint32_t r[kLoad];
+        tmem_load<kLoad>(tq + c, r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) red[(c + i) * kLM + f] = __uint_as_float(r[i]);
+        for (int i = 0; i < kLoad; ++i) red[(c + i) * kLM] = __uint_as_float(r[i]);
       }
     }
     if (splits > 1) fence_proxy_async_smem();  // read by the bulk copies
@@ -267,9 +273,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     // a wait gave up: every copy that was started lands, and every MMA ends,
     // before the shared and tensor memory are released (bounded)
     if (threadIdx.x == 0) {
-      const int n = *issued;
-      for (int s = 0; s < S && s < n; ++s)
-        mbar_wait_bounded(&full[s], last_armed_parity(n, S, s), a.status, kLDrainCycles);
+      const int started = *issued;
+      for (int s = 0; s < S && s < started; ++s)
+        mbar_wait_bounded(&full[s], last_armed_parity(started, S, s), a.status, kLDrainCycles);
       mbar_wait_bounded(tfull, 0, a.status, kLDrainCycles);
     }
     __syncthreads();
@@ -281,11 +287,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     tmem_dealloc(tbase, C::cols(S));
   }
   __syncwarp();
-  const uint8_t* sums = smem;
-  bool ok = true;
   if (splits > 1) {
     cluster_wait();
-    sums = smem + S * C::stride;
+    const uint8_t* sums = smem + S * C::stride;
     if ((int)threadIdx.x < splits) {
       const int to = threadIdx.x, count = min(per, nt - to * per);
       if (count > 0)
@@ -296,19 +300,20 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant
     __syncwarp();
     // not guarded by the abort flag: every rank sends, and what is on its way
     // here has to land before this CTA goes
-    ok = mbar_wait_bounded(joined, 0, a.status);
+    if (mbar_wait_bounded(joined, 0, a.status) && some) {
+      const float* at = reinterpret_cast<const float*>(sums) + threadIdx.x;
+      const int64_t y0 = (int64_t)(t0 + first) * a.ldy + n;
+      if (a.y_dtype == STRATA_DTYPE_F32)
+        write_joined<STRATA_DTYPE_F32>(a, at, y0, bias, mine, per, splits);
+      else if (a.y_dtype == STRATA_DTYPE_F16)
+        write_joined<STRATA_DTYPE_F16>(a, at, y0, bias, mine, per, splits);
+      else
+        write_joined<STRATA_DTYPE_BF16>(a, at, y0, bias, mine, per, splits);
+    }
     __syncwarp();
+    // nobody leaves while its sums are being sent
+    cluster_sync_relaxed();
   }
-  if (ok) {
-    if (a.y_dtype == STRATA_DTYPE_F32)
-      write_y<STRATA_DTYPE_F32>(a, sums, n0, t0 + first, mine, per, splits);
-    else if (a.y_dtype == STRATA_DTYPE_F16)
-      write_y<STRATA_DTYPE_F16>(a, sums, n0, t0 + first, mine, per, splits);
-    else
-      write_y<STRATA_DTYPE_BF16>(a, sums, n0, t0 + first, mine, per, splits);
-  }
-  __syncwarp();
-  if (splits > 1) cluster_sync_relaxed();  // nobody leaves while its sums are being sent
 }
 
 // Codes of a matrix as 128-byte (shared memory) x `box_rows` boxes.
