@@ -4,20 +4,20 @@
 // tensor cores: a tile of m x n reads (m + n) K elements from L2 for 2 m n K
 // operations, and the 148 SMs together get 11 to 13 TB/s.  So the tile is as
 // large as tensor memory allows: a pair of CTAs (cta_group::2) multiplies 256
-// tokens x 256 features, each CTA loading 128 rows of both and holding 128
-// tokens x 256 features of the sums.  T = 8192, N = 16384, K = 4096, 4x4 bits:
+// rows of A x 256 of B, each CTA loading 128 of both and holding 128 x 256 of
+// the sums.  T = 8192, N = 16384, K = 4096, 4x4 bits:
 // 431 us with 128 x 128 tiles of one CTA, 188 us (5.9 PFLOP/s) here; N =
 // 10240, K = 2560, 8x4 bits: 304 and 147 us (2.9 PFLOP/s); the tensor pipe is
 // active for 74 and 79 % of the cycles.  The order of the tiles makes no
 // difference (operands of this size stay in L2).
 //
 // Persistent: a pair takes tiles in turn.  Per CTA: warps 0-7 read the sums
-// out (a lane quarter of 32 tokens, half of the features each), warp 8 starts
+// out (a lane quarter of 32 rows of A, half of B's each), warp 8 starts
 // the copies, warp 9 of the even CTA issues the scale copies and the MMAs of
 // both.  The sums of a tile (256 columns) and the stages' scales (12 columns
 // per 128 of K) share the 512 columns, so the next tile waits until the
 // readers have the sums in registers (500 cycles after the last MMA); they are
-// rounded, turned in shared memory and stored while it runs.  Halves of 128
+// rounded and stored while it runs.  Halves of 128
 // features in three rotating buffers, which need not wait, are slower (229 us
 // when one buffer took 206): an MMA of 128 columns reads its other operand
 // twice as often.
@@ -34,28 +34,56 @@ namespace {
 constexpr int kGEpi = 8;                       // warps that read the sums
 constexpr int kGThreads = (kGEpi + 2) * 32;
 constexpr int kGM = 256, kGN = 256;            // a pair's tile
-constexpr int kGPitch = 69;                    // words between rows in store_shifted
 constexpr long long kGDrainCycles = 40000000LL;
 
-// ANY: rows of y need not start on 16-byte boundaries.
-template <int XF, int WF, bool ANY>
+// Which matrix is A decides what a lane of the tensor memory is when the sums
+// are read.  A feature (A = w): a token's 32 features are one store of the warp,
+// on any alignment, in few instructions.  A token (WIDE, A = x): rows are turned
+// in shared memory and stored 16 bytes a lane.  The first ends a tile sooner
+// (T = 1452, N = 25296, K = 640, 4x4 bits: 22 us for 29; T = 2048, N = K = 4096:
+// 16.0 for 17.3), the second takes less of the power that bounds long calls
+// (T = 8192, N = 10240, K = 2560, 8x4 bits, in a loop: 164 us for 173).
+template <int XF, int WF, bool WIDE>
 struct GemmCfg {
   static constexpr bool F4 = XF == STRATA_MX_FP4 && WF == STRATA_MX_FP4;
-  static constexpr bool kSpread = WF == STRATA_MX_FP4 && !F4;
-  static constexpr int KS = F4 ? 256 : 128, KI = F4 ? 64 : 32;
+  static constexpr int AF = WIDE ? XF : WF, BF = WIDE ? WF : XF;
+  static constexpr bool spread(int fmt) { return fmt == STRATA_MX_FP4 && !F4; }
+  static constexpr int KS = F4 ? 256 : 128;
   static constexpr int ST = KS / 128;
-  static constexpr int AB = 128 * 128, BB = 128 * 128;           // a CTA's rows of x and w
-  static constexpr int BTx = kSpread ? BB / 2 : BB;              // bytes read, spread or not
+  static constexpr int AB = 128 * 128;                           // a CTA's rows of A, and of B
+  static constexpr int tx(int fmt) { return spread(fmt) ? AB / 2 : AB; }  // bytes read
   static constexpr int SA = ST * kMxTileBytes, SBb = 2 * SA;     // scales of 128 and 256 rows
-  static constexpr int stage = AB + BB + SA + SBb;
+  static constexpr int stage = 2 * AB + SA + SBb;
   static constexpr int stride = (stage + 1023) / 1024 * 1024;
-  static constexpr int epi = kGEpi * 32 * (ANY ? 4 * kGPitch : 64);
-  static constexpr int bias = kGEpi * 128 * 4;
+  static constexpr int epi = WIDE ? kGEpi * 32 * 64 : 0;         // 64 bytes of 32 rows a warp
+  static constexpr int bias = WIDE ? kGEpi * 128 * 4 : 0;
   static constexpr int S = (227 * 1024 - 2048 - epi - bias) / stride;
   static constexpr int smem = S * stride + epi + bias + 2048;
   static constexpr int sfcols = 12 * ST;
+  // how the MMA's descriptor counts a format, and the map's x of a chunk
+  static constexpr uint32_t kind(int fmt) { return F4 ? 1u : fmt == STRATA_MX_FP4 ? 5u : 0u; }
+  STRATA_DEVFN static int at(int fmt, int ch) {
+    return spread(fmt) ? ch * KS : (int)mx_row_bytes(fmt, (int64_t)ch * KS);
+  }
   static_assert(kGN + S * sfcols <= 512, "sums and scales fit the tensor memory");
 };
+
+// 128 tokens of the lane's feature -> y, `count` of them y's, rows `pitch`
+// bytes apart.  A token's store is 32 features side by side, on any alignment.
+template <int DT, bool WHOLE>
+STRATA_DEVFN void store_tokens(uint8_t* y, int64_t pitch, const uint32_t (&r)[128], float bias,
+                               int count) {
+#pragma unroll
+  for (int k = 0; k < 128; ++k, y += pitch) {
+    const float v = __uint_as_float(r[k]) + bias;
+    if (WHOLE || k < count) {
+      if constexpr (DT == STRATA_DTYPE_F32)
+        *reinterpret_cast<float*>(y) = v;
+      else
+        *reinterpret_cast<uint16_t*>(y) = (uint16_t)pack2<DT>(v, v);
+    }
+  }
+}
 
 // A pass's 64 bytes of `rows` rows, a word a lane, side by side, where rows end
 // inside (`left` bytes of them are y's).
@@ -78,82 +106,18 @@ STRATA_DEVFN void store_rows(const uint8_t* buf, uint8_t* y, int64_t pitch, int 
   }
 }
 
-// Up to 256 bytes of 32 rows, a row a lane in w, to rows `pitch` apart that
-// start at y on any boundary of EL bytes: each row is shifted in shared memory
-// to how it lies in 16-byte pieces of memory, whole pieces are stored as such
-// and the (up to two) others element by element.  `left` bytes of a row are
-// y's.  Element by element throughout, the stores took longer than the MMAs:
-// T = 1452, N = 25295, K = 640, 4x4 bits 49 us, now 35 us, and 31 us with N =
-// 25296, whose rows are on 16-byte boundaries.
-template <int EL>
-STRATA_DEVFN void store_shifted(uint32_t* buf, const uint32_t* w, uint8_t* y, int64_t pitch,
-                                int rows, int left, int lane) {
-  left = min(left, 256);
-  if (left <= 0 || rows <= 0) return;
-  auto low = [&](int row) {  // where in a piece a row starts
-    return (int)((reinterpret_cast<uintptr_t>(y) + (uintptr_t)(row * pitch)) & 15);
-  };
-  {
-    const int s = low(lane);
-    // an odd number of 2-byte elements: words of the high half of one and the
-    // low half of the next
-    const bool half = EL == 2 && (s & 2);
-    const uint32_t sel = half ? 0x5432u : 0x7654u;
-    uint32_t* to = buf + lane * kGPitch + s / 4;
-    __syncwarp();
-    to[0] = __byte_perm(0u, w[0], sel);
-#pragma unroll
-    for (int i = 1; i < 64; ++i) to[i] = __byte_perm(w[i - 1], w[i], sel);
-    if (half) to[64] = w[63] >> 16;
-    __syncwarp();
-  }
-  // Whole pieces: 16 lanes a row (the 17th piece of a row is never whole).
-  {
-    const int pc = lane % 16;
-    uint8_t* at = y + (lane / 16) * pitch + pc * 16;
-    const uint32_t* v = buf + (lane / 16) * kGPitch + pc * 4;
-#pragma unroll 4
-    for (int row = lane / 16; row < 32; row += 2, at += 2 * pitch, v += 2 * kGPitch) {
-      const int s = low(row);
-      if (row < rows && pc * 16 >= s && pc * 16 + 16 <= s + left)
-        *reinterpret_cast<uint4*>(at - s) = make_uint4(v[0], v[1], v[2], v[3]);
-    }
-  }
-  // The others: a lane an element of a row's first or last piece, rows side by
-  // side (a row a lane cost the store unit 32 lines an instruction).
-  {
-    constexpr int kPiece = 16 / EL, kRows = 32 / (2 * kPiece);
-    const int end = lane % (2 * kPiece) / kPiece, e = lane % kPiece * EL;
-    uint8_t* to = y + lane / (2 * kPiece) * pitch;
-#pragma unroll 4
-    for (int row = lane / (2 * kPiece); row < 32; row += kRows, to += kRows * pitch) {
-      const int s = low(row), last = s + left;
-      const int at = (end ? last / 16 * 16 : 0) + e;  // from the row's first piece
-      // none: a whole first piece; a first piece that is the last; a whole last one
-      const bool some = end ? last % 16 != 0 : s != 0 && last >= 16;
-      if (row < rows && some && at >= s && at + EL <= last) {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(buf + row * kGPitch) + at;
-        if constexpr (EL == 4)
-          *reinterpret_cast<uint32_t*>(to + (at - s)) = *reinterpret_cast<const uint32_t*>(src);
-        else
-          *reinterpret_cast<uint16_t*>(to + (at - s)) = *reinterpret_cast<const uint16_t*>(src);
-      }
-    }
-  }
-}
-
-template <int XF, int WF, int DT, bool ANY>
+template <int XF, int WF, int DT, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
-mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-               const __grid_constant__ CUtensorMap xsmap, const __grid_constant__ CUtensorMap wsmap,
+mx_gemm_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+               const __grid_constant__ CUtensorMap asmap, const __grid_constant__ CUtensorMap bsmap,
                MxLinearArgs a, int mt, int tiles) {
-  using C = GemmCfg<XF, WF, ANY>;
+  using C = GemmCfg<XF, WF, WIDE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* epi = smem + C::S * C::stride;
   float* bias_s = reinterpret_cast<float*>(epi + C::epi);
-  uint64_t* full = reinterpret_cast<uint64_t*>(bias_s + C::bias / 4);
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi + C::epi + C::bias);
   uint64_t* empty = full + C::S;
   uint64_t* tfull = empty + C::S;
   uint64_t* tempty = tfull + 1;
@@ -197,19 +161,19 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     uint32_t ph = 1;
     bool ok = true;
     for (int tile = pair; tile < tiles && ok; tile += pairs) {
-      const int t0 = (tile % mt) * kGM, n0 = (tile / mt) * kGN;
+      const int tt = (tile % mt) * 256, tn = (tile / mt) * 256;  // its tokens and features
+      const int a0 = WIDE ? tt : tn, b0 = WIDE ? tn : tt;
       for (int ch = 0; ch < chunks; ++ch, ++i) {
         ok = __all_sync(0xffffffffu, mbar_wait_guarded(&empty[s], ph, a.status, abort_flag));
         if (!ok) break;
         uint8_t* st = smem + s * C::stride;
-        const int kx = (int)mx_row_bytes(XF, (int64_t)ch * C::KS);
-        const int kw = C::kSpread ? ch * C::KS : (int)mx_row_bytes(WF, (int64_t)ch * C::KS);
         load_stage_pair_warp(
-            rank == 0 ? &full[s] : nullptr, 2u * (C::AB + C::BTx + C::SA + C::SBb),
-            cluster_addr(smem_addr(&full[s]), 0), {&xmap, kx, t0 + 128 * (int)rank, st},
-            {&wmap, kw, n0 + 128 * (int)rank, st + C::AB},
-            {&xsmap, ch * C::ST * 64, t0 / 128 + (int)rank, st + C::AB + C::BB},
-            {&wsmap, ch * C::ST * 64, n0 / 128, st + C::AB + C::BB + C::SA});
+            rank == 0 ? &full[s] : nullptr, 2u * (C::tx(C::AF) + C::tx(C::BF) + C::SA + C::SBb),
+            cluster_addr(smem_addr(&full[s]), 0),
+            {&amap, C::at(C::AF, ch), a0 + 128 * (int)rank, st},
+            {&bmap, C::at(C::BF, ch), b0 + 128 * (int)rank, st + C::AB},
+            {&asmap, ch * C::ST * 64, a0 / 128 + (int)rank, st + 2 * C::AB},
+            {&bsmap, ch * C::ST * 64, b0 / 128, st + 2 * C::AB + C::SA});
         if (++s == C::S) s = 0, ph ^= 1u;
       }
     }
@@ -220,8 +184,6 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     if (rank == 0 && elect_one()) {
       const uint32_t hi = smem_desc_k128_hi(1024);
       const uint32_t smem0 = smem_addr(smem);
-      constexpr uint32_t xf = C::F4 ? 1u : XF == STRATA_MX_FP4 ? 5u : 0u;
-      constexpr uint32_t wf = C::F4 ? 1u : WF == STRATA_MX_FP4 ? 5u : 0u;
       int s = 0, it = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -234,17 +196,18 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           tc_fence_after();
           const int left = a.K - ch * C::KS;  // a multiple of 128
           const uint32_t st = smem0 + (uint32_t)(s * C::stride);
-          const uint32_t ssa = st + C::AB + C::BB, ssb = ssa + C::SA;
-          const uint32_t sfx = tbase + kGN + s * C::sfcols, sfw = sfx + 4 * C::ST;
-          const uint32_t xlo = smem_desc_k128_lo(st), wlo = smem_desc_k128_lo(st + C::AB);
+          const uint32_t ssa = st + 2 * C::AB, ssb = ssa + C::SA;
+          const uint32_t sfa = tbase + kGN + s * C::sfcols, sfb = sfa + 4 * C::ST;
+          const uint32_t alo = smem_desc_k128_lo(st), blo = smem_desc_k128_lo(st + C::AB);
 #pragma unroll
           for (int b = 0; b < C::ST; ++b) {
             if (b * 128 < left) {
-              const uint32_t sw = ssb + b * kMxTileBytes;  // of the first 128 features
+              const uint32_t sb = ssb + b * kMxTileBytes;  // of the first 128 rows of B
               mma_mx_block<C::F4, true>(
-                  tbase, xlo + 4 * b, wlo + 4 * b, hi, idesc_mx(xf, wf, kGM, kGN, 0), sfx + 4 * b,
-                  sfw + 8 * b, sfw + 8 * b, smem_desc_scale_lo(ssa + b * kMxTileBytes),
-                  smem_desc_scale_lo(sw), smem_desc_scale_lo(sw + C::SA), (uint32_t)(ch + b > 0));
+                  tbase, alo + 4 * b, blo + 4 * b, hi,
+                  idesc_mx(C::kind(C::AF), C::kind(C::BF), kGM, kGN, 0), sfa + 4 * b, sfb + 8 * b,
+                  sfb + 8 * b, smem_desc_scale_lo(ssa + b * kMxTileBytes), smem_desc_scale_lo(sb),
+                  smem_desc_scale_lo(sb + C::SA), (uint32_t)(ch + b > 0));
             }
           }
           mma_commit_pair(&empty[s]);
@@ -257,22 +220,26 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     __syncwarp();
   } else {
     // ------------------------------------------------ sums -> y
-    const int q = warp % 4, half = warp / 4;
-    uint8_t* buf = epi + warp * (C::epi / kGEpi);
+    const int q = warp % 4, half = warp / 4;  // 32 rows of A, 128 of B
     const uint32_t lead = cluster_addr(smem_addr(tempty), 0);
     constexpr int kEl = DT == STRATA_DTYPE_F32 ? 4 : 2;
-    constexpr int kPer = 64 / kEl;   // features a pass of aligned rows
+    constexpr int kPer = 64 / kEl;  // features a pass of WIDE
+    uint8_t* const buf = epi + warp * 32 * 64;
     int it = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++it) {
-      const int t0 = (tile % mt) * kGM + 128 * (int)rank + 32 * q;
-      const int n0 = (tile / mt) * kGN + 128 * half;
+      const int in_a = 128 * (int)rank + 32 * q, in_b = 128 * half;
+      const int t0 = (tile % mt) * 256 + (WIDE ? in_a : in_b);
+      const int n0 = (tile / mt) * 256 + (WIDE ? in_b : in_a);
+      float bias = 0.f;
       float* const bs = bias_s + warp * 128;
-      if (a.bias) {  // this warp's 128 features' while the MMAs run
+      if (WIDE && a.bias) {  // this warp's 128 features' while the MMAs run
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int n = n0 + 32 * i + lane;
           bs[32 * i + lane] = n < a.N ? a.bias[n] : 0.f;
         }
+      } else if (a.bias && n0 + lane < a.N) {
+        bias = a.bias[n0 + lane];
       }
       const bool ok = mbar_wait_guarded(tfull, it & 1, a.status, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -285,54 +252,58 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(lead);
-      if (a.bias) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float4 b = reinterpret_cast<const float4*>(bs)[i];
-          r[4 * i] = __float_as_uint(__uint_as_float(r[4 * i]) + b.x);
-          r[4 * i + 1] = __float_as_uint(__uint_as_float(r[4 * i + 1]) + b.y);
-          r[4 * i + 2] = __float_as_uint(__uint_as_float(r[4 * i + 2]) + b.z);
-          r[4 * i + 3] = __float_as_uint(__uint_as_float(r[4 * i + 3]) + b.w);
+      if constexpr (!WIDE) {
+        if (n0 + lane < a.N) {
+          uint8_t* const y = reinterpret_cast<uint8_t*>(a.y) + ((int64_t)t0 * a.ldy + n0 + lane) * kEl;
+          if (t0 + 128 <= a.T)
+            store_tokens<DT, true>(y, a.ldy * kEl, r, bias, 128);
+          else
+            store_tokens<DT, false>(y, a.ldy * kEl, r, bias, a.T - t0);
         }
-      }
-      if constexpr (kEl == 2) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-          r[i] = pack2<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-      }
-      const int rows = min(32, a.T - t0);
-      uint8_t* const yb = reinterpret_cast<uint8_t*>(a.y) + ((int64_t)t0 * a.ldy + n0) * kEl;
-      if constexpr (ANY) {
-#pragma unroll
-        for (int p = 0; p < kEl / 2; ++p)
-          store_shifted<kEl>(reinterpret_cast<uint32_t*>(buf), r + 64 * p, yb + 256 * p,
-                             a.ldy * kEl, rows, (a.N - n0) * kEl - 256 * p, lane);
-        continue;
-      }
-      // 64 bytes of each of the 32 rows at a time through shared memory, the
-      // 16-byte pieces of row r at places piece ^ (r/2 % 4): both the writes
-      // (a row a lane) and the reads (four lanes a row) touch every bank once
-      const bool whole = n0 + 128 <= a.N;
-      const int row = lane / 4, pc = lane % 4;
-#pragma unroll
-      for (int p = 0; p < 128 / kPer; ++p) {
         __syncwarp();
+      } else {
+        if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ (lane / 2)) & 3) * 16) =
-              make_uint4(r[16 * p + 4 * i], r[16 * p + 4 * i + 1], r[16 * p + 4 * i + 2],
-                         r[16 * p + 4 * i + 3]);
-        __syncwarp();
-        if (whole) {
+          for (int i = 0; i < 32; ++i) {
+            const float4 b = reinterpret_cast<const float4*>(bs)[i];
+            r[4 * i] = __float_as_uint(__uint_as_float(r[4 * i]) + b.x);
+            r[4 * i + 1] = __float_as_uint(__uint_as_float(r[4 * i + 1]) + b.y);
+            r[4 * i + 2] = __float_as_uint(__uint_as_float(r[4 * i + 2]) + b.z);
+            r[4 * i + 3] = __float_as_uint(__uint_as_float(r[4 * i + 3]) + b.w);
+          }
+        }
+        if constexpr (kEl == 2) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (g * 8 + row < rows)
-              *reinterpret_cast<uint4*>(yb + (int64_t)(g * 8 + row) * a.ldy * kEl + p * 64 +
-                                        pc * 16) =
-                  *reinterpret_cast<const uint4*>(buf + (g * 8 + row) * 64 +
-                                                  ((pc ^ (row / 2)) & 3) * 16);
-        } else {
-          store_rows<kEl>(buf, yb + p * 64, a.ldy * kEl, rows, (a.N - n0 - p * kPer) * kEl, lane);
+          for (int i = 0; i < 64; ++i)
+            r[i] = pack2<DT>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        }
+        const int rows = min(32, a.T - t0);
+        uint8_t* const yb = reinterpret_cast<uint8_t*>(a.y) + ((int64_t)t0 * a.ldy + n0) * kEl;
+        // 64 bytes of each of the 32 rows at a time through shared memory, the
+        // 16-byte pieces of row r at places piece ^ (r/2 % 4): both the writes
+        // (a row a lane) and the reads (four lanes a row) touch every bank once
+        const bool whole = n0 + 128 <= a.N;
+        const int row = lane / 4, pc = lane % 4;
+#pragma unroll
+        for (int p = 0; p < 128 / kPer; ++p) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ (lane / 2)) & 3) * 16) =
+                make_uint4(r[16 * p + 4 * i], r[16 * p + 4 * i + 1], r[16 * p + 4 * i + 2],
+                           r[16 * p + 4 * i + 3]);
+          __syncwarp();
+          if (whole) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (g * 8 + row < rows)
+                *reinterpret_cast<uint4*>(yb + (int64_t)(g * 8 + row) * a.ldy * kEl + p * 64 +
+                                          pc * 16) =
+                    *reinterpret_cast<const uint4*>(buf + (g * 8 + row) * 64 +
+                                                    ((pc ^ (row / 2)) & 3) * 16);
+          } else {
+            store_rows<kEl>(buf, yb + p * 64, a.ldy * kEl, rows, (a.N - n0 - p * kPer) * kEl, lane);
+          }
         }
       }
     }
@@ -377,18 +348,18 @@ bool make_scale_map(CUtensorMap* map, const uint8_t* scales, int rows, int K, in
                    CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <int XF, int WF, int DT, bool ANY>
+template <int XF, int WF, int DT, bool WIDE>
 cudaError_t launch_gemm(const MxLinearArgs& a, cudaStream_t st) {
-  using C = GemmCfg<XF, WF, ANY>;
+  using C = GemmCfg<XF, WF, WIDE>;
   CUtensorMap xmap, wmap, xsmap, wsmap;
-  if (!make_code_map(&xmap, a.x_codes, XF, false, a.T, a.K) ||
-      !make_code_map(&wmap, a.w_codes, WF, C::kSpread, a.N, a.K) ||
-      !make_scale_map(&xsmap, a.x_scales, a.T, a.K, C::ST, 1) ||
-      !make_scale_map(&wsmap, a.w_scales, a.N, a.K, C::ST, 2))
+  if (!make_code_map(&xmap, a.x_codes, XF, C::spread(XF), a.T, a.K) ||
+      !make_code_map(&wmap, a.w_codes, WF, C::spread(WF), a.N, a.K) ||
+      !make_scale_map(&xsmap, a.x_scales, a.T, a.K, C::ST, WIDE ? 1 : 2) ||
+      !make_scale_map(&wsmap, a.w_scales, a.N, a.K, C::ST, WIDE ? 2 : 1))
     return cudaErrorInvalidValue;
-  const int mt = (a.T + kGM - 1) / kGM, nt = (a.N + kGN - 1) / kGN;
+  const int mt = (a.T + 255) / 256, nt = (a.N + 255) / 256;
   const int tiles = mt * nt;
-  auto kern = mx_gemm_kernel<XF, WF, DT, ANY>;
+  auto kern = mx_gemm_kernel<XF, WF, DT, WIDE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -401,14 +372,21 @@ cudaError_t launch_gemm(const MxLinearArgs& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, xmap, wmap, xsmap, wsmap, a, mt, tiles);
+  return WIDE ? cudaLaunchKernelEx(&cfg, kern, xmap, wmap, xsmap, wsmap, a, mt, tiles)
+              : cudaLaunchKernelEx(&cfg, kern, wmap, xmap, wsmap, xsmap, a, mt, tiles);
 }
 
 template <int XF, int WF, int DT>
 cudaError_t launch_gemm_rows(const MxLinearArgs& a, cudaStream_t st) {
   constexpr int el = DT == STRATA_DTYPE_F32 ? 4 : 2;
+  // WIDE needs rows on 16-byte boundaries, and is for calls of many rounds of
+  // tiles that take longer to multiply than to store.
   const bool aligned = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy * el % 16 == 0;
-  return aligned ? launch_gemm<XF, WF, DT, false>(a, st) : launch_gemm<XF, WF, DT, true>(a, st);
+  const int64_t tiles = mx_ceil(a.T, 256) * mx_ceil(a.N, 256);
+  const int chunks = (int)mx_ceil(a.K, GemmCfg<XF, WF, true>::KS);
+  return aligned && tiles > 3 * (a.num_sms / 2) && chunks >= 8
+             ? launch_gemm<XF, WF, DT, true>(a, st)
+             : launch_gemm<XF, WF, DT, false>(a, st);
 }
 
 template <int XF, int WF>
