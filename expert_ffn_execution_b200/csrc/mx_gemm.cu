@@ -5,22 +5,21 @@
 // operations, and the 148 SMs together get 11 to 13 TB/s.  So the tile is as
 // large as tensor memory allows: a pair of CTAs (cta_group::2) multiplies 256
 // rows of A x 256 of B, each CTA loading 128 of both and holding 128 x 256 of
-// the sums.  T = 8192, N = 16384, K = 4096, 4x4 bits:
-// 431 us with 128 x 128 tiles of one CTA, 188 us (5.9 PFLOP/s) here; N =
-// 10240, K = 2560, 8x4 bits: 304 and 147 us (2.9 PFLOP/s); the tensor pipe is
-// active for 74 and 79 % of the cycles.  The order of the tiles makes no
-// difference (operands of this size stay in L2).
+// the sums.  T = 8192, N = 16384, K = 4096, 4x4 bits: 431 us with 128 x 128 tiles
+// of one CTA, 187 us (5.9 PFLOP/s) here; N = 10240, K = 2560, 8x4 bits: 304 and
+// 142 us (3.0 PFLOP/s); the tensor pipe is active for 74 and 79 % of the cycles.
+// In a loop of seconds power is the bound (216 and 166 us).  The order of the
+// tiles makes no difference (operands of this size stay in L2).
 //
 // Persistent: a pair takes tiles in turn.  Per CTA: warps 0-7 read the sums
-// out (a lane quarter of 32 rows of A, half of B's each), warp 8 starts
-// the copies, warp 9 of the even CTA issues the scale copies and the MMAs of
-// both.  The sums of a tile (256 columns) and the stages' scales (12 columns
+// out (a lane quarter of 32 rows of A, half of B's each), warp 8 starts the
+// copies, a lane of warp 9 of the even CTA issues the scale copies and the MMAs
+// of both.  The sums of a tile (256 columns) and the stages' scales (12 columns
 // per 128 of K) share the 512 columns, so the next tile waits until the
 // readers have the sums in registers (500 cycles after the last MMA); they are
-// rounded and stored while it runs.  Halves of 128
-// features in three rotating buffers, which need not wait, are slower (229 us
-// when one buffer took 206): an MMA of 128 columns reads its other operand
-// twice as often.
+// rounded and stored while it runs.  Halves of 128 columns in three rotating
+// buffers, which need not wait, are slower (229 us when one buffer took 206):
+// an MMA of 128 columns reads its other operand twice as often.
 #include <algorithm>
 
 #include "deal.h"

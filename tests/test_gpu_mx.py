@@ -378,6 +378,26 @@ def test_linear_same_bits_every_time_and_in_any_batch_of_a_tile():
         assert torch.equal(a, sm.mx_linear(x, w, out_dtype=torch.float32))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,N", [(3900, 4000), (4096, 4096), (3841, 4003), (4100, 3850)])
+@pytest.mark.parametrize("xf,wf,K", [(sm.MX_FP8, sm.MX_FP4, 1024), (sm.MX_FP4, sm.MX_FP4, 2176),
+                                     (sm.MX_FP8, sm.MX_FP8, 1152)])
+def test_linear_many_rounds_of_tiles(xf, wf, K, T, N, dtype):
+    """Small integers, exact in any order; rows of y further apart than they
+    are long, on 16-byte boundaries or not, and nothing behind them written."""
+    g = gen(71)
+    x = torch.randint(-3, 4, (T, K), device=DEV, generator=g).float()
+    w = torch.randint(-3, 4, (N, K), device=DEV, generator=g).float()
+    bias = torch.randint(-9, 10, (N,), device=DEV, generator=g).float()
+    want = (x @ w.T + bias).to(dtype)
+    q, wq = sm.mx_quantize(x, xf), sm.mx_quantize(w, wf)
+    for pitch in (N, N + 16 - N % 8, N + 1):
+        out = torch.full((T, pitch), 7, dtype=dtype, device=DEV)
+        sm.mx_linear(q, wq, bias, out=out[:, :N])
+        assert torch.equal(out[:, :N], want) and (out[:, N:] == 7).all()
+    assert torch.equal(sm.mx_linear(q, wq, out_dtype=dtype), (x @ w.T).to(dtype))
+
+
 @pytest.mark.parametrize("T", [1 << 22, (1 << 20) + 1])
 def test_linear_most_tokens(T):
     """Small integers, exact in any order; N too small for many tiles."""
