@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -58,12 +59,13 @@ def up_to_date() -> bool:
 
 
 def build_calls(force: bool = False) -> str:
-    deps = (CALLS_SRC, os.path.join(INCLUDE, "strata_moe.h"))
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    deps = (CALLS_SRC, os.path.join(INCLUDE, "strata_moe.h"), os.path.join(torch_dir, "version.py"))
     if not force and os.path.exists(CALLS) and all(
             os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
         return CALLS
     import torch  # its headers and libraries, which are loaded before the module is
-    at = os.path.join(os.path.dirname(torch.__file__), "include")
+    at = os.path.join(torch_dir, "include")
     libs = ("c10", "c10_cuda", "torch_cpu", "torch_cuda", "torch_python")
     cuda = os.path.dirname(os.path.dirname(NVCC))
     cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-Wall", "-shared", "-fPIC",
@@ -71,7 +73,7 @@ def build_calls(force: bool = False) -> str:
            f'-DSTRATA_TORCH="{torch.__version__}"', "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
            "-isystem", at, "-isystem", os.path.join(at, "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), CALLS_SRC, "-o", CALLS + ".tmp",
-           "-L", os.path.join(os.path.dirname(at), "lib"), *("-l" + n for n in libs)]
+           "-L", os.path.join(torch_dir, "lib"), *("-l" + n for n in libs)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stderr}")
