@@ -483,9 +483,9 @@ STRATA_API int32_t moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* d
  *   dev_status may be NULL.
  * A row of x or w with a NaN block or code gives NaN in its outputs; products
  * beyond fp32's range become infinite, those below it may vanish.  y overlaps
- * no input.  The sums'
- * order depends on (T, N, K), the formats and the device alone: the same
- * bits on every run.  No workspace.
+ * no input.  The order of the sums depends on (T, N, K), the formats, whether
+ * y's rows are on 16-byte boundaries, and the device alone: the same bits on
+ * every run.  No workspace.
  * Limits: T >= 0 (0: no-op) up to 2^22, N >= 1, K a multiple of 128, at least
  * 128, N and K up to 2^24. */
 STRATA_API int32_t moe_mx_linear(const void* x_codes, int32_t x_fmt, const void* x_scales, int32_t T,
