@@ -16,6 +16,7 @@ call, which then runs here.
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import NamedTuple
 
 import torch
@@ -107,8 +108,7 @@ def _check_format(fmt, rows, K, layout):
                          "both below 2^31, are wanted")
 
 
-_FIELDS = ("fmt", "layout", "rows", "K", "codes_ptr", "scales_ptr", "index", "device", "_both",
-           "_codes", "_scales")
+_FIELDS = ("_fmt", "_layout", "_rows", "_K", "_both", "_codes", "_scales")
 if _mxcalls is not None:
     _Matrix = _mxcalls.Matrix  # these fields, natively
 else:
@@ -119,7 +119,11 @@ else:
 class MXTensor(_Matrix):
     """A microscaled matrix [rows, K] on the device: uint8 codes [rows, K/2]
     (MX_FP4) or [rows, K] (MX_FP8) and uint8 scales, [rows, K/32] (MX_ROWS) or
-    the flat plane of tiles that mx_linear reads (MX_TILES)."""
+    the flat plane of tiles that mx_linear reads (MX_TILES).
+
+    It holds the two tensors, not their addresses: every call looks at where
+    they are when it is made, and refuses them if they no longer fit.  Copies
+    and pickles have tensors of their own."""
 
     __slots__ = ()
 
@@ -128,30 +132,25 @@ class MXTensor(_Matrix):
         if _fast and _fast.wrap(self, codes, scales, fmt, rows, K, layout):
             return
         _check_format(fmt, rows, K, layout)
-        for t, n, what in ((codes, _code_bytes(rows, fmt, K), "codes"),
-                           (scales, _scale_bytes(rows, K, layout), "scales")):
-            if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n:
-                raise ValueError(f"{what} must be contiguous uint8 of {n} bytes")
-        self.device, self.index = codes.device, codes.get_device()
-        if scales.device != self.device:
-            raise ValueError(f"codes on {self.device} and scales on {scales.device}")
-        self.fmt, self.rows, self.K, self.layout = fmt, rows, K, layout
+        self._fmt, self._rows, self._K, self._layout = fmt, rows, K, layout
         self._codes, self._scales, self._both = codes, scales, None
-        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+        _planes(self)
 
     @classmethod
     def _empty(cls, fmt: int, rows: int, K: int, layout: int, dev) -> MXTensor:
         """One to be written by a call: both planes in one allocation."""
         _check_format(fmt, rows, K, layout)
         q = cls.__new__(cls)
-        q.fmt, q.rows, q.K, q.layout = fmt, rows, K, layout
-        q.device, q.index = dev, dev.index
-        at = (_code_bytes(rows, fmt, K) + 255) & ~255
-        q._both = torch.empty(at + _scale_bytes(rows, K, layout), dtype=torch.uint8, device=dev)
+        q._fmt, q._rows, q._K, q._layout = fmt, rows, K, layout
+        n = _scales_at(q) + _scale_bytes(rows, K, layout)
+        q._both = torch.empty(n, dtype=torch.uint8, device=dev)
         q._codes = q._scales = None
-        q.codes_ptr = q._both.data_ptr()
-        q.scales_ptr = q.codes_ptr + at
         return q
+
+    def __reduce__(self):
+        return type(self), (self.codes, self.scales, self.fmt, self.rows, self.K, self.layout)
+
+    fmt, layout, rows, K = (property(operator.attrgetter(n)) for n in _FIELDS[:4])
 
     @property
     def codes(self) -> torch.Tensor:
@@ -164,9 +163,21 @@ class MXTensor(_Matrix):
     def scales(self) -> torch.Tensor:
         if self._scales is None:
             n = _scale_bytes(self.rows, self.K, self.layout)
-            s = self._both[self.scales_ptr - self.codes_ptr:][:n]
+            s = self._both[_scales_at(self):][:n]
             self._scales = s.view(self.rows, self.K // 32) if self.layout == B.MX_ROWS else s
         return self._scales
+
+    @property
+    def device(self) -> torch.device:
+        return (self._both if self._codes is None else self._codes).device
+
+    @property
+    def index(self) -> int:
+        """Of the CUDA device, -1: none."""
+        return (self._both if self._codes is None else self._codes).get_device()
+
+    codes_ptr = property(lambda self: _planes(self)[0])
+    scales_ptr = property(lambda self: _planes(self)[1])
 
     def dequantize(self, dtype=torch.float32, stream=None) -> torch.Tensor:
         """The matrix's values: [rows, K] of `dtype`."""
@@ -176,12 +187,32 @@ class MXTensor(_Matrix):
         if _elsewhere(dev):
             with torch.cuda.device(dev):
                 return self.dequantize(dtype, stream)
+        codes, scales = _planes(self)
         lib, stream = _enter(dev, stream)
         out = torch.empty(self.rows, self.K, dtype=dtype, device=dev)
-        rc = lib.moe_mx_dequantize(self.codes_ptr, 0, self.scales_ptr, self.layout, 0, self.fmt, 1,
-                                   self.rows, self.K, out.data_ptr(), dt, self.K, 0, stream)
+        rc = lib.moe_mx_dequantize(codes, 0, scales, self.layout, 0, self.fmt, 1, self.rows, self.K,
+                                   out.data_ptr(), dt, self.K, 0, stream)
         _check("moe_mx_dequantize", rc)
         return out
+
+
+def _scales_at(q: MXTensor) -> int:
+    """Where the scales are in one allocation of both planes."""
+    return (_code_bytes(q.rows, q.fmt, q.K) + 255) & ~255
+
+
+def _planes(q: MXTensor):
+    """Where the codes and the scales are now.  The tensors may have been given
+    other memory since the last call (`t.data = ...`, Module.to())."""
+    codes, scales = q._codes, q._scales
+    for t, n, what in ((codes, _code_bytes(q.rows, q.fmt, q.K), "codes"),
+                       (scales, _scale_bytes(q.rows, q.K, q.layout), "scales")):
+        if t is not None and (t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n):
+            raise ValueError(f"{what} must be contiguous uint8 of {n} bytes")
+    a, b = (q._both if t is None else t for t in (codes, scales))
+    if a.device != b.device:
+        raise ValueError(f"codes on {a.device} and scales on {b.device}")
+    return a.data_ptr(), b.data_ptr() + (_scales_at(q) if scales is None else 0)
 
 
 def mx_quantize(x: torch.Tensor, fmt: int, layout: int = B.MX_TILES, stream=None) -> MXTensor:
@@ -204,8 +235,9 @@ def mx_quantize(x: torch.Tensor, fmt: int, layout: int = B.MX_TILES, stream=None
             return mx_quantize(x, fmt, layout, stream)
     lib, stream = _enter(dev, stream)
     q = MXTensor._empty(fmt, rows, K, layout, dev)
-    rc = lib.moe_mx_quantize(ptr, dt, 1, rows, K, stride, 0, fmt, q.codes_ptr, 0, q.scales_ptr,
-                             layout, 0, stream)
+    codes, scales = _planes(q)
+    rc = lib.moe_mx_quantize(ptr, dt, 1, rows, K, stride, 0, fmt, codes, 0, scales, layout, 0,
+                             stream)
     _check("moe_mx_quantize", rc)
     return q
 
@@ -220,7 +252,7 @@ def mx_tile_scales(q: MXTensor, stream=None) -> MXTensor:
             return mx_tile_scales(q, stream)
     lib, stream = _enter(dev, stream)
     tiles = torch.empty(_scale_bytes(q.rows, q.K, B.MX_TILES), dtype=torch.uint8, device=dev)
-    rc = lib.moe_mx_tile_scales(q.scales_ptr, q.rows, q.K, tiles.data_ptr(), stream)
+    rc = lib.moe_mx_tile_scales(_planes(q)[1], q.rows, q.K, tiles.data_ptr(), stream)
     _check("moe_mx_tile_scales", rc)
     return MXTensor(q.codes, tiles, q.fmt, q.rows, q.K, B.MX_TILES)
 
@@ -270,9 +302,9 @@ def add_rmsnorm(x: torch.Tensor, delta: torch.Tensor | None = None,
         res = torch.empty_like(x)
     out = None if out_dtype is None else torch.empty(T, H, dtype=out_dtype, device=dev)
     q = MXTensor._empty(fmt, T, H, layout, dev) if fmt else None
+    codes, scales = _planes(q) if fmt else (None, None)
     rc = lib.moe_add_rmsnorm(x.data_ptr(), xd, _ptr(delta), dd, _ptr(gain), T, H, eps, _ptr(res),
-                             _ptr(out), od, fmt, q.codes_ptr if fmt else None,
-                             q.scales_ptr if fmt else None, layout, stream)
+                             _ptr(out), od, fmt, codes, scales, layout, stream)
     _check("moe_add_rmsnorm", rc)
     return AddNorm(x if res is None else res, out, q)
 
@@ -310,8 +342,9 @@ def mx_linear(x: MXTensor, w: MXTensor, bias: torch.Tensor | None = None,
     lib, stream = _enter(dev, stream)
     if out is None:
         out = torch.empty(T, N, dtype=out_dtype, device=dev)
-    rc = lib.moe_mx_linear(x.codes_ptr, x.fmt, x.scales_ptr, T, w.codes_ptr, w.fmt, w.scales_ptr,
-                           N, K, _ptr(bias), out.data_ptr(), dt, ldy, _ptr(dev_status), stream)
+    (xc, xs), (wc, ws) = _planes(x), _planes(w)
+    rc = lib.moe_mx_linear(xc, x.fmt, xs, T, wc, w.fmt, ws, N, K, _ptr(bias), out.data_ptr(), dt,
+                           ldy, _ptr(dev_status), stream)
     _check("moe_mx_linear", rc)
     return out
 

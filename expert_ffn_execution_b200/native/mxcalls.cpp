@@ -22,7 +22,6 @@
 #include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
-#include <torch/csrc/Device.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -48,7 +47,6 @@ PyObject* torch_param;     // torch.nn.Parameter
 PyTypeObject* matrix_type; // Matrix below
 PyTypeObject* mx_type;     // mx.py's MXTensor, a subclass of it
 PyTypeObject* norm_type;   // mx.py's AddNorm, a named tuple
-PyObject* devices[64];     // torch.device("cuda", i), as they are met
 PyObject* s_cuda_stream;   // an interned name
 
 // ---------------------------------------------------------------- MXTensor's fields
@@ -56,11 +54,8 @@ struct Matrix {
   PyObject_HEAD
   int fmt, layout;
   Py_ssize_t rows, K;
-  unsigned long long codes_ptr, scales_ptr;
-  int index;  // of the CUDA device, -1: none
-  PyObject* device;
-  at::Tensor both;           // one allocation for both planes, or
-  PyObject *codes, *scales;  // the two planes' tensors
+  at::Tensor both;           // one allocation for both planes
+  PyObject *codes, *scales;  // a plane's tensor, where it has one of its own or was asked for
 };
 
 PyObject* matrix_new(PyTypeObject* type, PyObject*, PyObject*) {
@@ -72,14 +67,12 @@ PyObject* matrix_new(PyTypeObject* type, PyObject*, PyObject*) {
 int matrix_traverse(PyObject* o, visitproc visit, void* arg) {
   Matrix* m = reinterpret_cast<Matrix*>(o);
   Py_VISIT(Py_TYPE(o));
-  Py_VISIT(m->device);
   Py_VISIT(m->codes);
   Py_VISIT(m->scales);
   return 0;
 }
 int matrix_clear(PyObject* o) {
   Matrix* m = reinterpret_cast<Matrix*>(o);
-  Py_CLEAR(m->device);
   Py_CLEAR(m->codes);
   Py_CLEAR(m->scales);
   return 0;
@@ -93,14 +86,10 @@ void matrix_dealloc(PyObject* o) {
   Py_DECREF(type);
 }
 PyMemberDef matrix_members[] = {
-    {"fmt", T_INT, offsetof(Matrix, fmt), 0, nullptr},
-    {"layout", T_INT, offsetof(Matrix, layout), 0, nullptr},
-    {"rows", T_PYSSIZET, offsetof(Matrix, rows), 0, nullptr},
-    {"K", T_PYSSIZET, offsetof(Matrix, K), 0, nullptr},
-    {"codes_ptr", T_ULONGLONG, offsetof(Matrix, codes_ptr), 0, nullptr},
-    {"scales_ptr", T_ULONGLONG, offsetof(Matrix, scales_ptr), 0, nullptr},
-    {"index", T_INT, offsetof(Matrix, index), 0, nullptr},
-    {"device", T_OBJECT, offsetof(Matrix, device), 0, nullptr},
+    {"_fmt", T_INT, offsetof(Matrix, fmt), 0, nullptr},
+    {"_layout", T_INT, offsetof(Matrix, layout), 0, nullptr},
+    {"_rows", T_PYSSIZET, offsetof(Matrix, rows), 0, nullptr},
+    {"_K", T_PYSSIZET, offsetof(Matrix, K), 0, nullptr},
     {"_codes", T_OBJECT, offsetof(Matrix, codes), 0, nullptr},
     {"_scales", T_OBJECT, offsetof(Matrix, scales), 0, nullptr},
     {nullptr, 0, 0, 0, nullptr}};
@@ -182,8 +171,6 @@ bool read(PyObject* o, Tensor* t) {
   return true;
 }
 
-bool is_mx(PyObject* o) { return Py_TYPE(o) == mx_type; }
-
 // The stream's handle on device `index`, which has to be the current one.
 bool target(int index, PyObject* stream, void** handle) {
   if (c10::impl::TorchDispatchModeTLS::any_modes_set() || c10::cuda::current_device() != index)
@@ -201,12 +188,6 @@ bool target(int index, PyObject* stream, void** handle) {
   return true;
 }
 
-PyObject* device_object(int index) {  // borrowed
-  if (!devices[index])
-    devices[index] = THPDevice_New(at::Device(at::kCUDA, (c10::DeviceIndex)index));
-  return devices[index];
-}
-
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type, int index) {
   return at::Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, (c10::DeviceIndex)index),
                                            std::nullopt));
@@ -222,31 +203,72 @@ bool format(long fmt, int64_t rows, int64_t K, long layout) {
          K >= 32 && K < 1LL << 31 && K % 32 == 0;
 }
 
+// Where the scales are in one allocation of both planes.
+int64_t scales_at(int fmt, int64_t rows, int64_t K) {
+  return (code_bytes(rows, fmt, K) + 255) & ~(int64_t)255;
+}
+
+// An MXTensor as it is now.  Its tensors may have been given other memory
+// since the last call, so each call asks them, as mx.py's _planes().
+struct Mx {
+  int fmt, layout, index;
+  int64_t rows, K;
+  uint8_t *codes, *scales;
+};
+bool plane(const Tensor& t, int64_t bytes) {
+  if (t.dtype != 8) return false;
+  if (t.dims == 1) return t.size[0] == bytes && (bytes <= 1 || t.stride[0] == 1);
+  return t.rows_contiguous() && t.size[0] * t.size[1] == bytes;
+}
+bool read_mx(PyObject* o, Mx* q) {
+  if (Py_TYPE(o) != mx_type) return false;
+  const Matrix& m = *reinterpret_cast<Matrix*>(o);
+  if (!format(m.fmt, m.rows, m.K, m.layout)) return false;
+  q->fmt = m.fmt;
+  q->layout = m.layout;
+  q->rows = m.rows;
+  q->K = m.K;
+  int index[2];
+  PyObject* own[2] = {m.codes, m.scales};
+  uint8_t** at[2] = {&q->codes, &q->scales};
+  const int64_t bytes[2] = {code_bytes(m.rows, m.fmt, m.K), scale_bytes(m.rows, m.K, m.layout)};
+  const int64_t offset[2] = {0, scales_at(m.fmt, m.rows, m.K)};
+  for (int i = 0; i < 2; ++i) {
+    if (own[i] && own[i] != Py_None) {
+      Tensor t;
+      if (!read(own[i], &t) || !plane(t, bytes[i])) return false;
+      index[i] = t.index;
+      *at[i] = static_cast<uint8_t*>(t.ptr);
+    } else {
+      if (!m.both.defined() || !m.both.is_cuda()) return false;
+      index[i] = m.both.device().index();
+      *at[i] = static_cast<uint8_t*>(m.both.data_ptr()) + offset[i];
+    }
+  }
+  q->index = index[0];
+  return index[0] == index[1];
+}
+
 // Memory for an MXTensor that a call writes, both planes in one allocation.
 struct Planes {
   at::Tensor both;
   uint8_t *codes = nullptr, *scales = nullptr;
   Planes() = default;
   Planes(int fmt, int64_t rows, int64_t K, int layout, int index) {
-    const int64_t at = (code_bytes(rows, fmt, K) + 255) & ~(int64_t)255;
+    const int64_t at = scales_at(fmt, rows, K);
     both = empty({at + scale_bytes(rows, K, layout)}, at::kByte, index);
     codes = static_cast<uint8_t*>(both.data_ptr());
     scales = codes + at;
   }
 };
-PyObject* new_matrix(Planes&& p, int fmt, int64_t rows, int64_t K, int layout, int index) {
-  PyObject* dev = device_object(index);
-  PyObject* o = dev ? matrix_new(mx_type, nullptr, nullptr) : nullptr;
+PyObject* new_matrix(Planes&& p, int fmt, int64_t rows, int64_t K, int layout) {
+  PyObject* o = matrix_new(mx_type, nullptr, nullptr);
   if (!o) return nullptr;
   Matrix* m = reinterpret_cast<Matrix*>(o);
   m->fmt = fmt;
   m->layout = layout;
   m->rows = rows;
   m->K = K;
-  m->index = index;
-  m->device = Py_NewRef(dev);
-  m->codes_ptr = reinterpret_cast<uintptr_t>(p.codes);
-  m->scales_ptr = reinterpret_cast<uintptr_t>(p.scales);
   m->both = std::move(p.both);
   return o;
 }
@@ -307,36 +329,25 @@ PyObject* quantize(PyObject* const* args, Py_ssize_t n) {  // x, fmt, layout, st
                         (int32_t)fmt, p.codes, 0, p.scales, (int32_t)layout, 0, stream);
   });
   if (rc != STRATA_OK) NOT_TAKEN;
-  return new_matrix(std::move(p), (int)fmt, x.size[0], x.size[1], (int)layout, x.index);
+  return new_matrix(std::move(p), (int)fmt, x.size[0], x.size[1], (int)layout);
 }
 
 // q, codes, scales, fmt, rows, K, layout: fills in q; True where it did.
 PyObject* wrap(PyObject* const* args, Py_ssize_t n) {
   Tensor codes, scales;
   long fmt, rows, K, layout;
-  if (n != 7 || !is_mx(args[0]) || !small_int(args[3], &fmt) || !small_int(args[4], &rows) ||
-      !small_int(args[5], &K) || !small_int(args[6], &layout) || !format(fmt, rows, K, layout) ||
-      !read(args[1], &codes) || !read(args[2], &scales))
+  if (n != 7 || Py_TYPE(args[0]) != mx_type || !small_int(args[3], &fmt) ||
+      !small_int(args[4], &rows) || !small_int(args[5], &K) || !small_int(args[6], &layout) ||
+      !format(fmt, rows, K, layout) || !read(args[1], &codes) || !read(args[2], &scales) ||
+      codes.index != scales.index || !plane(codes, code_bytes(rows, (int)fmt, K)) ||
+      !plane(scales, scale_bytes(rows, K, (int)layout)))
     NOT_TAKEN;
-  auto plane = [](const Tensor& t, int64_t bytes) {
-    if (t.dims == 1) return t.size[0] == bytes && (bytes <= 1 || t.stride[0] == 1);
-    return t.rows_contiguous() && t.size[0] * t.size[1] == bytes;
-  };
-  if (codes.dtype != 8 || scales.dtype != 8 || codes.index != scales.index ||
-      !plane(codes, code_bytes(rows, (int)fmt, K)) || !plane(scales, scale_bytes(rows, K, (int)layout)))
-    NOT_TAKEN;
-  PyObject* dev = device_object(codes.index);
-  if (!dev) return nullptr;
   Matrix* m = reinterpret_cast<Matrix*>(args[0]);
   m->fmt = (int)fmt;
   m->layout = (int)layout;
   m->rows = rows;
   m->K = K;
-  m->index = codes.index;
-  m->codes_ptr = reinterpret_cast<uintptr_t>(codes.ptr);
-  m->scales_ptr = reinterpret_cast<uintptr_t>(scales.ptr);
   m->both = at::Tensor();
-  Py_XSETREF(m->device, Py_NewRef(dev));
   Py_XSETREF(m->codes, Py_NewRef(args[1]));
   Py_XSETREF(m->scales, Py_NewRef(args[2]));
   Py_RETURN_TRUE;
@@ -344,17 +355,15 @@ PyObject* wrap(PyObject* const* args, Py_ssize_t n) {
 
 PyObject* dequantize(PyObject* const* args, Py_ssize_t n) {  // q, dtype, stream
   void* stream;
-  if (n != 3 || !is_mx(args[0])) NOT_TAKEN;
-  const Matrix& m = *reinterpret_cast<Matrix*>(args[0]);
+  Mx q;
+  if (n != 3 || !read_mx(args[0], &q)) NOT_TAKEN;
   const int dt = dtype_of(args[1]);
-  if (dt < 0 || !m.device || m.device == Py_None || m.index < 0 || !target(m.index, args[2], &stream))
-    NOT_TAKEN;
+  if (dt < 0 || !target(q.index, args[2], &stream)) NOT_TAKEN;
   at::Tensor out;
   const int32_t rc = launch([&] {
-    out = empty({(int64_t)m.rows, (int64_t)m.K}, scalar_type(dt), m.index);
-    return lib.dequantize(reinterpret_cast<const void*>(m.codes_ptr), 0,
-                          reinterpret_cast<const void*>(m.scales_ptr), m.layout, 0, m.fmt, 1,
-                          (int32_t)m.rows, (int32_t)m.K, out.data_ptr(), dt, m.K, 0, stream);
+    out = empty({q.rows, q.K}, scalar_type(dt), q.index);
+    return lib.dequantize(q.codes, 0, q.scales, q.layout, 0, q.fmt, 1, (int32_t)q.rows, (int32_t)q.K,
+                          out.data_ptr(), dt, q.K, 0, stream);
   });
   if (rc != STRATA_OK) NOT_TAKEN;
   return THPVariable_Wrap(std::move(out));
@@ -407,7 +416,7 @@ PyObject* add_rmsnorm(PyObject* const* args, Py_ssize_t n) {
   if (one) {
     PyObject* a = has_res ? Py_NewRef(args[7]) : has_delta ? THPVariable_Wrap(std::move(r)) : Py_NewRef(args[0]);
     PyObject* b = has_out ? THPVariable_Wrap(std::move(out)) : Py_NewRef(Py_None);
-    PyObject* c = fmt ? new_matrix(std::move(p), (int)fmt, x.size[0], x.size[1], (int)layout, x.index)
+    PyObject* c = fmt ? new_matrix(std::move(p), (int)fmt, x.size[0], x.size[1], (int)layout)
                       : Py_NewRef(Py_None);
     PyTuple_SET_ITEM(parts, 0, a);
     PyTuple_SET_ITEM(parts, 1, b);
@@ -421,12 +430,11 @@ PyObject* add_rmsnorm(PyObject* const* args, Py_ssize_t n) {
 
 // x, w, bias, out_dtype, out, dev_status, stream
 PyObject* linear(PyObject* const* args, Py_ssize_t n) {
-  if (n != 7 || !is_mx(args[0]) || !is_mx(args[1])) NOT_TAKEN;
-  const Matrix &x = *reinterpret_cast<Matrix*>(args[0]), &w = *reinterpret_cast<Matrix*>(args[1]);
+  Mx x, w;
+  if (n != 7 || !read_mx(args[0], &x) || !read_mx(args[1], &w)) NOT_TAKEN;
   Tensor bias, out, status;
   void* stream;
-  if (x.K != w.K || x.layout != STRATA_MX_TILES || w.layout != STRATA_MX_TILES || x.index < 0 ||
-      x.index != w.index)
+  if (x.K != w.K || x.layout != STRATA_MX_TILES || w.layout != STRATA_MX_TILES || x.index != w.index)
     NOT_TAKEN;
   const bool has_bias = args[2] != Py_None, has_out = args[4] != Py_None;
   if (has_bias && (!read(args[2], &bias) || bias.dtype != 0 || bias.index != x.index ||
@@ -449,15 +457,12 @@ PyObject* linear(PyObject* const* args, Py_ssize_t n) {
   at::Tensor y;
   const int32_t rc = launch([&] {
     if (!has_out) {
-      y = empty({(int64_t)x.rows, (int64_t)w.rows}, scalar_type(dt), x.index);
+      y = empty({x.rows, w.rows}, scalar_type(dt), x.index);
       out.ptr = y.data_ptr();
     }
-    return lib.linear(reinterpret_cast<const void*>(x.codes_ptr), x.fmt,
-                      reinterpret_cast<const void*>(x.scales_ptr), (int32_t)x.rows,
-                      reinterpret_cast<const void*>(w.codes_ptr), w.fmt,
-                      reinterpret_cast<const void*>(w.scales_ptr), (int32_t)w.rows, (int32_t)w.K,
-                      static_cast<const float*>(bias.ptr), out.ptr, dt, ldy,
-                      static_cast<int32_t*>(status.ptr), stream);
+    return lib.linear(x.codes, x.fmt, x.scales, (int32_t)x.rows, w.codes, w.fmt, w.scales,
+                      (int32_t)w.rows, (int32_t)w.K, static_cast<const float*>(bias.ptr), out.ptr,
+                      dt, ldy, static_cast<int32_t*>(status.ptr), stream);
   });
   if (rc != STRATA_OK) NOT_TAKEN;
   return has_out ? Py_NewRef(args[4]) : THPVariable_Wrap(std::move(y));

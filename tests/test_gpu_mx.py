@@ -4,7 +4,9 @@ Quantised codes and scales, and values read back, are compared bit for bit:
 the format determines them.  Tolerances elsewhere are counted in half steps
 (2^-8 for bf16, 2^-11 for fp16, 2^-24 for fp32) as each test derives."""
 import concurrent.futures
+import copy
 import gc
+import io
 import sys
 
 import numpy as np
@@ -815,3 +817,36 @@ def test_native_expert_calls_leave_refusals_to_python():
             (lambda: e.dequantize(torch.int32), TypeError, "dtype")):
         with pytest.raises(error, match=match):
             call()
+
+
+# ---------------------------------------------------------------- a matrix's memory
+@pytest.mark.parametrize("fast", [True, False])
+def test_matrix_follows_its_tensors(monkeypatch, fast):
+    """Calls read a matrix where it is: copied, saved, given other memory."""
+    x, w = torch.randn(5, 256, device=DEV, generator=gen(90)), torch.randn(70, 256, device=DEV, generator=gen(91))
+    if not fast:
+        monkeypatch.setattr(mx, "_fast", None)
+        monkeypatch.setattr(mx, "_mxcalls", None)
+    q = sm.mx_quantize(x, sm.MX_FP8)
+    v = q.dequantize()
+    for made in (sm.mx_quantize(w, sm.MX_FP4), sm.mx_tile_scales(sm.mx_quantize(w, sm.MX_FP4, sm.MX_ROWS))):
+        want, values = sm.mx_linear(q, made), made.dequantize()
+        other = sm.mx_quantize(2 * w, sm.MX_FP4)
+        twice = sm.mx_linear(q, other)
+        r = copy.deepcopy(made)
+        p = sm.MXTensor(torch.nn.Parameter(made.codes.clone(), requires_grad=False),
+                        torch.nn.Parameter(made.scales.clone(), requires_grad=False), sm.MX_FP4, 70, 256, sm.MX_TILES)
+        made.codes.zero_()
+        assert torch.equal(sm.mx_linear(q, r), want) and torch.equal(r.dequantize(), values)
+        assert torch.equal(sm.mx_linear(q, p), want)
+        for m in (r, p):
+            m.codes.data, m.scales.data = other.codes.clone(), other.scales.clone()
+            assert torch.equal(sm.mx_linear(q, m), twice) and torch.equal(m.dequantize(), 2 * values)
+            m.codes.data = m.codes.data[:64]
+            for call in (m.dequantize, lambda: sm.mx_linear(q, m)):
+                with pytest.raises(ValueError, match="codes must be"):
+                    call()
+    f = io.BytesIO()
+    torch.save(q, f)
+    f.seek(0)
+    assert torch.equal(torch.load(f, weights_only=False).dequantize(), v)

@@ -1,6 +1,10 @@
 """CPU checks of the microscaled operators: the C entry points refuse bad
 arguments before anything is enqueued, the torch-level calls refuse what the
 library could not read, and the reference the GPU tests use is pinned."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -228,3 +232,77 @@ def test_torch_level_refusals():
     e = sm.ExpertWeights(torch.zeros(2, 1 << 17, dtype=torch.uint8), sm.FMT_Q2_32, 256, 128)
     with pytest.raises(ValueError, match="MXFP4"):
         e.dequantize()
+
+
+# ---------------------------------------------------------------- a matrix's memory
+HELD = """
+import copy, io, pickle, sys
+if {plain}:
+    sys.modules["expert_ffn_execution_b200._mxcalls"] = None
+import torch
+import expert_ffn_execution_b200 as sm
+from expert_ffn_execution_b200 import mx
+assert (mx._mxcalls is None) == {plain}
+
+
+def make():
+    c = torch.randint(0, 256, (4, 64), dtype=torch.uint8)
+    s = torch.randint(0, 256, (4, 4), dtype=torch.uint8)
+    return sm.MXTensor(c, s, sm.MX_FP4, 4, 128, sm.MX_ROWS)
+
+
+def whole(q):
+    assert q.codes_ptr == q.codes.data_ptr() and q.scales_ptr == q.scales.data_ptr()
+    assert (q.fmt, q.layout, q.rows, q.K, q.index, q.device.type) == (sm.MX_FP4, sm.MX_ROWS, 4, 128, -1, "cpu")
+
+
+def refuses(error, f, *a):
+    try:
+        f(*a)
+    except error:
+        return
+    raise AssertionError("not refused")
+
+
+both = sm.MXTensor._empty(sm.MX_FP4, 4, 128, sm.MX_ROWS, torch.device("cpu"))
+assert both.scales_ptr == both.codes_ptr + 256
+both.codes.copy_(torch.arange(256).view(4, 64) % 251)
+both.scales.fill_(120)
+for q in (make(), both):
+    whole(q)
+    f = io.BytesIO()
+    torch.save(q, f)
+    f.seek(0)
+    for r in (copy.deepcopy(q), pickle.loads(pickle.dumps(q)), torch.load(f, weights_only=False)):
+        whole(r)
+        assert torch.equal(r.codes, q.codes) and torch.equal(r.scales, q.scales)
+        assert r.codes_ptr != q.codes_ptr and r.scales_ptr != q.scales_ptr
+    r = copy.copy(q)
+    whole(r)
+    assert r.codes is q.codes and r.scales is q.scales
+    # other memory of the same form is followed, another form refused
+    q.codes.data = torch.zeros(4, 64, dtype=torch.uint8)
+    q.scales.data = torch.zeros(4, 4, dtype=torch.uint8)
+    whole(q)
+    for t, bad in ((q.codes, torch.zeros(3, 64, dtype=torch.uint8)), (q.scales, torch.zeros(4, 4)),
+                   (q.codes, torch.zeros(4, 128, dtype=torch.uint8)[:, ::2])):
+        kept = t.data
+        t.data = bad
+        refuses(ValueError, mx._planes, q)
+        t.data = kept
+        whole(q)
+    for n in ("fmt", "layout", "rows", "K"):
+        refuses(AttributeError, setattr, q, n, 1000)
+    whole(q)
+"""
+
+
+@pytest.mark.parametrize("plain", [False, True])
+def test_matrix_follows_its_tensors(plain):
+    """Copied, saved, given other memory: a matrix's addresses are those of its
+    tensors, with the native fields and without."""
+    if not plain:
+        pytest.importorskip("expert_ffn_execution_b200._mxcalls")
+    r = subprocess.run([sys.executable, "-c", HELD.format(plain=plain)], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
