@@ -57,6 +57,13 @@ struct LinCfg {
   static constexpr int smem(int S, bool split) {
     return S * stride + head + 1024 + (split ? NT * token : 0);
   }
+  // The most that any call of the kernel asks for.  What a kernel may ask for is
+  // the process's, not the call's: set to less for one call, it would be too
+  // little for another thread's.
+  static constexpr int kMost =
+      std::max(std::max(smem(stages(kAlone, false), false), smem(stages(kAlone, true), true)),
+               std::max(smem(stages(kShared, false), false), smem(stages(kShared, true), true)));
+  static_assert(kMost <= 227 * 1024, "what an SM has for a CTA");
   static constexpr int cols(int S) {
     return dcols + S * sfcols <= 64 ? 64 : dcols + S * sfcols <= 128 ? 128 : 256;
   }
@@ -343,7 +350,7 @@ cudaError_t launch_linear(const MxLinearArgs& a, int splits, cudaStream_t st) {
   const bool alone = splits <= 2 && (int64_t)tn * tt * splits <= a.num_sms;
   const int S = C::stages(alone ? C::kAlone : C::kShared, split);
   auto kern = mx_linear_kernel<XF, WF, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(S, split));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kMost);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];

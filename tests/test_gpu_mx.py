@@ -8,6 +8,7 @@ import copy
 import gc
 import io
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -850,3 +851,33 @@ def test_matrix_follows_its_tensors(monkeypatch, fast):
     torch.save(q, f)
     f.seek(0)
     assert torch.equal(torch.load(f, weights_only=False).dequantize(), v)
+
+
+# ---------------------------------------------------------------- calls of several threads
+def test_linear_of_several_threads_and_shapes():
+    """Products of one tile width that want different amounts of shared memory,
+    side by side: the amount is a property of the kernel, not of the call."""
+    shapes = [(4, 128, 128), (4, 4100, 2560), (4, 40000, 128), (4, 2560, 8192)]
+    made = []
+    for i, (T, N, K) in enumerate(shapes):
+        x, _ = random_mx(T, K, sm.MX_FP8, 100 + i)
+        w, _ = random_mx(N, K, sm.MX_FP4, 200 + i)
+        y = torch.empty(T, N, device=DEV)
+        made.append((x, w, y, sm.mx_linear(x, w, out_dtype=torch.float32)))
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(shapes))
+
+    def calls(i):
+        (T, N, K), (x, w, y, _) = shapes[i], made[i]
+        torch.cuda.synchronize()  # the device is this thread's too
+        stream = torch.cuda.Stream().cuda_stream
+        a = (x.codes, sm.MX_FP8, x.scales, T, w.codes, sm.MX_FP4, w.scales, N, K, None, y, sm.DTYPE_F32, N, None)
+        start.wait()
+        return [rc for _ in range(4000) if (rc := sm.moe_mx_linear(*a, stream, check=False))]
+
+    with concurrent.futures.ThreadPoolExecutor(len(shapes)) as pool:
+        failed = list(pool.map(calls, range(len(shapes))))
+    torch.cuda.synchronize()
+    assert failed == [[]] * len(shapes)
+    for *_, y, want in made:
+        assert torch.equal(y, want)
