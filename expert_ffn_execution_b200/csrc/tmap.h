@@ -28,6 +28,13 @@ inline EncodeTiledFn encode_tiled() {
   return fn;
 }
 
+// The driver's encoder wants a current context, which a host thread has only
+// once it has used the device: makes the runtime's current device the thread's.
+inline bool adopt_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
 // Tiled map of a rank-`rank` tensor: dims[0] innermost (contiguous), byte
 // strides of dims 1..rank-1, box extents per dim.  Returns false when the
 // encoder is unavailable or rejects the description (alignment, extents).
@@ -37,10 +44,14 @@ inline bool make_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, con
   EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  const CUresult r =
-      enc(map, dtype, (cuuint32_t)rank, const_cast<void*>(base), dims, byte_strides, box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encode = [&] {
+    return enc(map, dtype, (cuuint32_t)rank, const_cast<void*>(base), dims, byte_strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if ((r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) && adopt_device())
+    r = encode();
   return r == CUDA_SUCCESS;
 }
 

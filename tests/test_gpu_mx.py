@@ -881,3 +881,16 @@ def test_linear_of_several_threads_and_shapes():
     assert failed == [[]] * len(shapes)
     for *_, y, want in made:
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,N,K", [(4, 300, 256), (200, 300, 256), (2000, 2048, 1024)])
+def test_linear_from_a_thread_that_has_not_used_the_device(T, N, K):
+    x, _ = random_mx(T, K, sm.MX_FP8, 110)
+    w, _ = random_mx(N, K, sm.MX_FP4, 111)
+    want = sm.mx_linear(x, w)
+    out = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    with concurrent.futures.ThreadPoolExecutor(1) as pool:
+        pool.submit(sm.mx_linear, x, w, out=out).result()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
