@@ -3,8 +3,9 @@ devices, allocate the outputs and call the library on the tensors' device and
 that device's current stream (or `stream`).  No arithmetic happens here, and
 nothing is recorded for a backward pass.
 
-A tensor that is used on another stream than the one it was made on is the
-caller's to order and to keep alive, as with any asynchronous call.
+What a call makes belongs to the stream that it runs on, also where that is
+given by `stream`.  A tensor that is used on another stream than the one it was
+made on is the caller's to order and to keep alive, as with any asynchronous call.
 
 A decode step's kernels take a few microseconds, so the host's part of a call
 counts.  The codes and scales that a call makes share one allocation, their
@@ -66,19 +67,29 @@ def _device(first, *others):
     return dev
 
 
-def _enter(dev, stream):
-    """(library, stream handle) for a call on `dev`, which must be current:
-    `stream` as a handle, or the device's current stream."""
+def _place(dev, stream):
+    """A context in which `dev` and `stream` (a stream, its handle, or None)
+    are current, or None where they are.  What a call allocates is then the
+    stream's that writes it: memory that another stream has given back may
+    still be that stream's to use."""
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    return _library(), stream
+        return None if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if dev.index == torch._C._cuda_getDevice() and \
+            handle == torch._C._cuda_getCurrentRawStream(dev.index):
+        return None
+    if getattr(stream, "device", dev) != dev:
+        raise ValueError(f"tensors on {dev} and a stream of {stream.device}")
+    if handle in (0, 1):  # the default stream, by its two handles
+        return torch.cuda.stream(torch.cuda.default_stream(dev))
+    if handle == 2:
+        raise ValueError("the threads' default stream is not one that torch allocates for")
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, dev))
 
 
-def _elsewhere(dev) -> bool:
-    """Whether `dev` is not the current device."""
-    return dev.index != torch._C._cuda_getDevice()
+def _enter(dev):
+    """(library, stream handle) for a call on `dev`, which is current."""
+    return _library(), torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _check(name, rc):
@@ -184,11 +195,11 @@ class MXTensor(_Matrix):
         if _fast and (out := _fast.dequantize(self, dtype, stream)) is not None:
             return out
         dt, dev = _dtype(dtype), _device(self)
-        if _elsewhere(dev):
-            with torch.cuda.device(dev):
-                return self.dequantize(dtype, stream)
+        if (place := _place(dev, stream)) is not None:
+            with place:
+                return self.dequantize(dtype)
         codes, scales = _planes(self)
-        lib, stream = _enter(dev, stream)
+        lib, stream = _enter(dev)
         out = torch.empty(self.rows, self.K, dtype=dtype, device=dev)
         rc = lib.moe_mx_dequantize(codes, 0, scales, self.layout, 0, self.fmt, 1, self.rows, self.K,
                                    out.data_ptr(), dt, self.K, 0, stream)
@@ -230,10 +241,10 @@ def mx_quantize(x: torch.Tensor, fmt: int, layout: int = B.MX_TILES, stream=None
     if K < 32 or K % 32:
         raise ValueError(f"K = {K}: a positive multiple of 32 is wanted")
     dev = _device(x)
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return mx_quantize(x, fmt, layout, stream)
-    lib, stream = _enter(dev, stream)
+    if (place := _place(dev, stream)) is not None:
+        with place:
+            return mx_quantize(x, fmt, layout)
+    lib, stream = _enter(dev)
     q = MXTensor._empty(fmt, rows, K, layout, dev)
     codes, scales = _planes(q)
     rc = lib.moe_mx_quantize(ptr, dt, 1, rows, K, stride, 0, fmt, codes, 0, scales, layout, 0,
@@ -247,10 +258,10 @@ def mx_tile_scales(q: MXTensor, stream=None) -> MXTensor:
     if q.layout == B.MX_TILES:
         return q
     dev = _device(q)
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return mx_tile_scales(q, stream)
-    lib, stream = _enter(dev, stream)
+    if (place := _place(dev, stream)) is not None:
+        with place:
+            return mx_tile_scales(q)
+    lib, stream = _enter(dev)
     tiles = torch.empty(_scale_bytes(q.rows, q.K, B.MX_TILES), dtype=torch.uint8, device=dev)
     rc = lib.moe_mx_tile_scales(_planes(q)[1], q.rows, q.K, tiles.data_ptr(), stream)
     _check("moe_mx_tile_scales", rc)
@@ -293,10 +304,10 @@ def add_rmsnorm(x: torch.Tensor, delta: torch.Tensor | None = None,
     xd, dd = _dtype(x.dtype), 0 if delta is None else _dtype(delta.dtype)
     od = 0 if out_dtype is None else _dtype(out_dtype)
     dev = _device(x, delta, gain, residual_out)
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return add_rmsnorm(x, delta, gain, eps, out_dtype, fmt, layout, residual_out, stream)
-    lib, stream = _enter(dev, stream)
+    if (place := _place(dev, stream)) is not None:
+        with place:
+            return add_rmsnorm(x, delta, gain, eps, out_dtype, fmt, layout, residual_out)
+    lib, stream = _enter(dev)
     res = residual_out
     if res is None and delta is not None:
         res = torch.empty_like(x)
@@ -336,10 +347,10 @@ def mx_linear(x: MXTensor, w: MXTensor, bias: torch.Tensor | None = None,
             ldy = out.stride(0)
     dt = _dtype(out_dtype)
     dev = _device(x, w, bias, out, dev_status)
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return mx_linear(x, w, bias, out_dtype, out, dev_status, stream)
-    lib, stream = _enter(dev, stream)
+    if (place := _place(dev, stream)) is not None:
+        with place:
+            return mx_linear(x, w, bias, out_dtype, out, dev_status)
+    lib, stream = _enter(dev)
     if out is None:
         out = torch.empty(T, N, dtype=out_dtype, device=dev)
     (xc, xs), (wc, ws) = _planes(x), _planes(w)
@@ -371,10 +382,10 @@ def pack_experts(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
             raise ValueError("weights must have contiguous rows that start on 16-byte boundaries")
         rows.append(row)
         experts.append(expert)
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return pack_experts(gate, up, down, stream)
-    _, stream = _enter(dev, stream)
+    if (place := _place(dev, stream)) is not None:
+        with place:
+            return pack_experts(gate, up, down)
+    _, stream = _enter(dev)
     blobs = torch.empty(E, B.strata_expert_bytes(B.FMT_MXFP4_32, H, I), dtype=torch.uint8, device=dev)
     B.moe_mx_pack_experts(gate, up, down, dt, rows, experts, E, H, I, blobs, blobs.stride(0),
                           stream)
@@ -388,10 +399,10 @@ def unpack_experts(w: ExpertWeights, dtype=torch.float32, stream=None):
     if _fast and (made := _fast.unpack(w.blobs, w.hidden, w.inter, dtype, stream)) is not None:
         return made
     dt, dev, E, H, I = _dtype(dtype), _device(w.blobs), w.num_experts, w.hidden, w.inter
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
-            return unpack_experts(w, dtype, stream)
-    _, stream = _enter(dev, stream)
+    if (place := _place(dev, stream)) is not None:
+        with place:
+            return unpack_experts(w, dtype)
+    _, stream = _enter(dev)
     gate = torch.empty(E, I, H, dtype=dtype, device=dev)
     up = torch.empty(E, I, H, dtype=dtype, device=dev)
     down = torch.empty(E, H, I, dtype=dtype, device=dev)

@@ -21,12 +21,14 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
 #include <new>
+#include <optional>
 
 #include "strata_moe.h"
 
@@ -47,7 +49,7 @@ PyObject* torch_param;     // torch.nn.Parameter
 PyTypeObject* matrix_type; // Matrix below
 PyTypeObject* mx_type;     // mx.py's MXTensor, a subclass of it
 PyTypeObject* norm_type;   // mx.py's AddNorm, a named tuple
-PyObject* s_cuda_stream;   // an interned name
+PyObject *s_cuda_stream, *s_device_index;  // interned names
 
 // ---------------------------------------------------------------- MXTensor's fields
 struct Matrix {
@@ -171,20 +173,40 @@ bool read(PyObject* o, Tensor* t) {
   return true;
 }
 
-// The stream's handle on device `index`, which has to be the current one.
-bool target(int index, PyObject* stream, void** handle) {
+bool address(PyObject* o, void** p) {
+  const unsigned long long v = PyLong_Check(o) ? PyLong_AsUnsignedLongLong(o) : 0;
+  if (v == ~0ull && PyErr_Occurred()) return pass();
+  *p = reinterpret_cast<void*>(v);
+  return PyLong_Check(o);
+}
+
+// Where a call runs: on device `index`, which has to be the current one, on
+// the current stream or, where the call names another, on that one, which is
+// then the current one while the call allocates and launches (mx.py's _place()).
+struct Target {
+  void* handle = nullptr;
+  std::optional<c10::cuda::CUDAStream> other;
+};
+bool target(int index, PyObject* stream, Target* to) {
   if (c10::impl::TorchDispatchModeTLS::any_modes_set() || c10::cuda::current_device() != index)
     return false;
-  if (stream == Py_None) {
-    *handle = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
-    return true;
+  to->handle = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
+  if (stream == Py_None) return true;
+  void* handle = nullptr;
+  if (PyLong_Check(stream)) {
+    if (!address(stream, &handle)) return false;
+  } else {
+    PyObject* s = PyObject_GetAttr(stream, s_cuda_stream);
+    PyObject* of = s ? PyObject_GetAttr(stream, s_device_index) : nullptr;
+    const bool fits = of && PyLong_Check(of) && PyLong_AsLong(of) == index && address(s, &handle);
+    Py_XDECREF(s);
+    Py_XDECREF(of);
+    if (!fits) return pass();
   }
-  PyObject* s = PyLong_Check(stream) ? Py_NewRef(stream) : PyObject_GetAttr(stream, s_cuda_stream);
-  if (!s) return pass();
-  const long long v = PyLong_AsLongLong(s);
-  Py_DECREF(s);
-  if (v == -1 && PyErr_Occurred()) return pass();
-  *handle = reinterpret_cast<void*>(v);
+  if (handle == to->handle) return true;
+  if (reinterpret_cast<uintptr_t>(handle) < 4096) return false;  // a default stream's handle
+  to->handle = handle;
+  to->other = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), (c10::DeviceIndex)index);
   return true;
 }
 
@@ -277,10 +299,12 @@ PyObject* new_matrix(Planes&& p, int fmt, int64_t rows, int64_t K, int layout) {
 // call may wait for the allocator or the device).  Anything but STRATA_OK, an
 // exception among it, leaves the call to mx.py.
 template <typename F>
-int32_t launch(F f) {
+int32_t launch(const Target& to, F f) {
   int32_t rc = STRATA_ECUDA;
   Py_BEGIN_ALLOW_THREADS
   try {
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    if (to.other) guard.reset_stream(*to.other);
     rc = f();
   } catch (const std::exception&) {
   }
@@ -316,17 +340,17 @@ bool small_int(PyObject* o, long* v) {
 PyObject* quantize(PyObject* const* args, Py_ssize_t n) {  // x, fmt, layout, stream
   Tensor x;
   long fmt, layout;
-  void* stream;
+  Target to;
   if (n != 4 || !small_int(args[1], &fmt) || !small_int(args[2], &layout) || !read(args[0], &x) ||
       x.dims != 2 || x.dtype > 2 || !format(fmt, x.size[0], x.size[1], layout) ||
-      !target(x.index, args[3], &stream))
+      !target(x.index, args[3], &to))
     NOT_TAKEN;
   if (x.size[0] > 0 && x.stride[1] != 1) NOT_TAKEN;
   Planes p;
-  const int32_t rc = launch([&] {
+  const int32_t rc = launch(to, [&] {
     p = Planes((int)fmt, x.size[0], x.size[1], (int)layout, x.index);
     return lib.quantize(x.ptr, x.dtype, 1, (int32_t)x.size[0], (int32_t)x.size[1], x.stride[0], 0,
-                        (int32_t)fmt, p.codes, 0, p.scales, (int32_t)layout, 0, stream);
+                        (int32_t)fmt, p.codes, 0, p.scales, (int32_t)layout, 0, to.handle);
   });
   if (rc != STRATA_OK) NOT_TAKEN;
   return new_matrix(std::move(p), (int)fmt, x.size[0], x.size[1], (int)layout);
@@ -354,16 +378,16 @@ PyObject* wrap(PyObject* const* args, Py_ssize_t n) {
 }
 
 PyObject* dequantize(PyObject* const* args, Py_ssize_t n) {  // q, dtype, stream
-  void* stream;
+  Target to;
   Mx q;
   if (n != 3 || !read_mx(args[0], &q)) NOT_TAKEN;
   const int dt = dtype_of(args[1]);
-  if (dt < 0 || !target(q.index, args[2], &stream)) NOT_TAKEN;
+  if (dt < 0 || !target(q.index, args[2], &to)) NOT_TAKEN;
   at::Tensor out;
-  const int32_t rc = launch([&] {
+  const int32_t rc = launch(to, [&] {
     out = empty({q.rows, q.K}, scalar_type(dt), q.index);
     return lib.dequantize(q.codes, 0, q.scales, q.layout, 0, q.fmt, 1, (int32_t)q.rows, (int32_t)q.K,
-                          out.data_ptr(), dt, q.K, 0, stream);
+                          out.data_ptr(), dt, q.K, 0, to.handle);
   });
   if (rc != STRATA_OK) NOT_TAKEN;
   return THPVariable_Wrap(std::move(out));
@@ -373,7 +397,7 @@ PyObject* dequantize(PyObject* const* args, Py_ssize_t n) {  // q, dtype, stream
 PyObject* add_rmsnorm(PyObject* const* args, Py_ssize_t n) {
   Tensor x, delta, gain, res;
   long fmt, layout;
-  void* stream;
+  Target to;
   if (n != 9 || !PyFloat_Check(args[3]) || !small_int(args[5], &fmt) || !small_int(args[6], &layout) ||
       !read(args[0], &x) || x.dtype > 2 || !x.rows_contiguous() || x.size[0] >= 1LL << 31 ||
       x.size[1] >= 1LL << 31)
@@ -392,11 +416,11 @@ PyObject* add_rmsnorm(PyObject* const* args, Py_ssize_t n) {
                    gain.dims != 1 || gain.size[0] != x.size[1] ||
                    (gain.size[0] > 1 && gain.stride[0] != 1)))
     NOT_TAKEN;
-  if (!target(x.index, args[8], &stream)) NOT_TAKEN;
+  if (!target(x.index, args[8], &to)) NOT_TAKEN;
   const float eps = (float)PyFloat_AS_DOUBLE(args[3]);
   at::Tensor r, out;
   Planes p;
-  const int32_t rc = launch([&] {
+  const int32_t rc = launch(to, [&] {
     if (has_delta && !has_res) {
       r = empty({x.size[0], x.size[1]}, scalar_type(x.dtype), x.index);
       res.ptr = r.data_ptr();
@@ -406,7 +430,7 @@ PyObject* add_rmsnorm(PyObject* const* args, Py_ssize_t n) {
     return lib.add_rmsnorm(x.ptr, x.dtype, delta.ptr, has_delta ? delta.dtype : 0,
                            static_cast<const float*>(gain.ptr), (int32_t)x.size[0],
                            (int32_t)x.size[1], eps, res.ptr, has_out ? out.data_ptr() : nullptr, od,
-                           (int32_t)fmt, p.codes, p.scales, (int32_t)layout, stream);
+                           (int32_t)fmt, p.codes, p.scales, (int32_t)layout, to.handle);
   });
   if (rc != STRATA_OK) NOT_TAKEN;
   // AddNorm((residual, out, mx)), by the tuple's constructor
@@ -433,7 +457,7 @@ PyObject* linear(PyObject* const* args, Py_ssize_t n) {
   Mx x, w;
   if (n != 7 || !read_mx(args[0], &x) || !read_mx(args[1], &w)) NOT_TAKEN;
   Tensor bias, out, status;
-  void* stream;
+  Target to;
   if (x.K != w.K || x.layout != STRATA_MX_TILES || w.layout != STRATA_MX_TILES || x.index != w.index)
     NOT_TAKEN;
   const bool has_bias = args[2] != Py_None, has_out = args[4] != Py_None;
@@ -453,16 +477,16 @@ PyObject* linear(PyObject* const* args, Py_ssize_t n) {
     dt = out.dtype;
     if (x.rows > 1) ldy = out.stride[0];
   }
-  if (dt < 0 || !target(x.index, args[6], &stream)) NOT_TAKEN;
+  if (dt < 0 || !target(x.index, args[6], &to)) NOT_TAKEN;
   at::Tensor y;
-  const int32_t rc = launch([&] {
+  const int32_t rc = launch(to, [&] {
     if (!has_out) {
       y = empty({x.rows, w.rows}, scalar_type(dt), x.index);
       out.ptr = y.data_ptr();
     }
     return lib.linear(x.codes, x.fmt, x.scales, (int32_t)x.rows, w.codes, w.fmt, w.scales,
                       (int32_t)w.rows, (int32_t)w.K, static_cast<const float*>(bias.ptr), out.ptr,
-                      dt, ldy, static_cast<int32_t*>(status.ptr), stream);
+                      dt, ldy, static_cast<int32_t*>(status.ptr), to.handle);
   });
   if (rc != STRATA_OK) NOT_TAKEN;
   return has_out ? Py_NewRef(args[4]) : THPVariable_Wrap(std::move(y));
@@ -470,7 +494,7 @@ PyObject* linear(PyObject* const* args, Py_ssize_t n) {
 
 PyObject* pack(PyObject* const* args, Py_ssize_t n) {  // gate, up, down, stream: the blobs
   Tensor w[3];
-  void* stream;
+  Target to;
   if (n != 4) NOT_TAKEN;
   int64_t rows[3], experts[3];
   for (int i = 0; i < 3; ++i) {
@@ -483,15 +507,15 @@ PyObject* pack(PyObject* const* args, Py_ssize_t n) {  // gate, up, down, stream
   const int64_t E = w[0].size[0], I = w[0].size[1], H = w[0].size[2];
   if (E < 1 || I < 128 || H < 128 || E >> 31 || I >> 31 || H >> 31 || w[1].size[0] != E ||
       w[1].size[1] != I || w[1].size[2] != H || w[2].size[0] != E || w[2].size[1] != H ||
-      w[2].size[2] != I || !target(w[0].index, args[3], &stream))
+      w[2].size[2] != I || !target(w[0].index, args[3], &to))
     NOT_TAKEN;
   at::Tensor blobs;
-  const int32_t rc = launch([&] {
+  const int32_t rc = launch(to, [&] {
     const int64_t bytes = (int64_t)lib.expert_bytes(STRATA_FMT_MXFP4_32, (int32_t)H, (int32_t)I);
     if (!bytes) return (int32_t)STRATA_EINVAL;
     blobs = empty({E, bytes}, at::kByte, w[0].index);
     return lib.pack(w[0].ptr, w[1].ptr, w[2].ptr, w[0].dtype, rows, experts, (int32_t)E, (int32_t)H,
-                    (int32_t)I, blobs.data_ptr(), (uint64_t)bytes, stream);
+                    (int32_t)I, blobs.data_ptr(), (uint64_t)bytes, to.handle);
   });
   if (rc != STRATA_OK) NOT_TAKEN;
   return THPVariable_Wrap(std::move(blobs));
@@ -500,20 +524,20 @@ PyObject* pack(PyObject* const* args, Py_ssize_t n) {  // gate, up, down, stream
 PyObject* unpack(PyObject* const* args, Py_ssize_t n) {  // blobs, H, I, dtype, stream
   Tensor b;
   long H, I;
-  void* stream;
+  Target to;
   if (n != 5 || !read(args[0], &b) || b.dims != 2 || b.dtype != 8 || b.stride[1] != 1 ||
       b.size[0] >> 31 || !small_int(args[1], &H) || !small_int(args[2], &I) || H < 128 || I < 128 ||
       H >> 31 || I >> 31)
     NOT_TAKEN;
   const int dt = dtype_of(args[3]);
-  if (dt < 0 || !target(b.index, args[4], &stream)) NOT_TAKEN;
+  if (dt < 0 || !target(b.index, args[4], &to)) NOT_TAKEN;
   at::Tensor w[3];
-  const int32_t rc = launch([&] {
+  const int32_t rc = launch(to, [&] {
     for (int i = 0; i < 3; ++i)
       w[i] = i < 2 ? empty({b.size[0], I, H}, scalar_type(dt), b.index)
                    : empty({b.size[0], H, I}, scalar_type(dt), b.index);
     return lib.unpack(b.ptr, (uint64_t)b.stride[0], (int32_t)b.size[0], (int32_t)H, (int32_t)I,
-                      w[0].data_ptr(), w[1].data_ptr(), w[2].data_ptr(), dt, stream);
+                      w[0].data_ptr(), w[1].data_ptr(), w[2].data_ptr(), dt, to.handle);
   });
   if (rc != STRATA_OK) NOT_TAKEN;
   PyObject* all = PyTuple_New(3);
@@ -574,10 +598,11 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_mxcalls",
 
 PyMODINIT_FUNC PyInit__mxcalls(void) {
   s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
+  s_device_index = PyUnicode_InternFromString("device_index");
   PyObject* m = PyModule_Create(&module_def);
   PyObject* type = PyType_FromSpec(&matrix_spec);
   matrix_type = reinterpret_cast<PyTypeObject*>(type);
-  if (!m || !type || !s_cuda_stream || PyModule_AddObject(m, "Matrix", type) < 0 ||
+  if (!m || !type || !s_cuda_stream || !s_device_index || PyModule_AddObject(m, "Matrix", type) < 0 ||
       PyModule_AddStringConstant(m, "torch_version", STRATA_TORCH) < 0)
     return nullptr;
   return m;

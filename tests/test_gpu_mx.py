@@ -894,3 +894,70 @@ def test_linear_from_a_thread_that_has_not_used_the_device(T, N, K):
         pool.submit(sm.mx_linear, x, w, out=out).result()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+# ---------------------------------------------------------------- a stream that is not the current one
+def owner(t):
+    """The stream whose memory a tensor is in."""
+    at = t.data_ptr()
+    return next(s["stream"] for s in torch.cuda.memory_snapshot()
+                if s["address"] <= at < s["address"] + s["total_size"])
+
+
+@pytest.mark.parametrize("fast", [True, False])
+def test_results_are_the_streams_that_writes_them(monkeypatch, fast):
+    """Memory that the current stream has given back may still be written by
+    what it has yet to do: a call on another stream takes none of it."""
+    if not fast:
+        monkeypatch.setattr(mx, "_fast", None)
+        monkeypatch.setattr(mx, "_mxcalls", None)
+    x, d = (torch.randn(5, 256, device=DEV, generator=gen(120 + i)) for i in range(2))
+    gate = torch.randn(2, 128, 256, device=DEV, generator=gen(122))
+    down = torch.randn(2, 256, 128, device=DEV, generator=gen(123))
+
+    def every(stream):
+        q = sm.mx_quantize(x, sm.MX_FP8, stream=stream)
+        r = sm.mx_tile_scales(sm.mx_quantize(x, sm.MX_FP8, sm.MX_ROWS, stream=stream), stream)
+        n = sm.add_rmsnorm(x, d, out_dtype=torch.float16, fmt=sm.MX_FP4, stream=stream)
+        e = sm.pack_experts(gate, gate, down, stream)
+        return [q.codes, q.scales, q.dequantize(stream=stream), r.scales, n.residual, n.out, n.mx.codes,
+                sm.mx_linear(q, r, stream=stream), e.blobs, *e.dequantize(stream=stream)]
+
+    want = every(None)
+    torch.cuda.synchronize()
+    current, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    assert all(owner(t) == current.cuda_stream for t in want)
+    for stream in (side, side.cuda_stream):
+        got = every(stream)
+        torch.cuda.synchronize()
+        assert torch.cuda.current_stream() == current
+        for a, b in zip(got, want):
+            assert owner(a) == side.cuda_stream and a.shape == b.shape and a.dtype == b.dtype
+            assert a.dtype == torch.uint8 or torch.equal(a, b)
+    with torch.cuda.stream(side):  # the default stream by its handles, from another one
+        for handle in (0, 1, torch.cuda.default_stream()):
+            got = every(handle)
+            torch.cuda.synchronize()
+            assert all(owner(t) == 0 for t in got) and torch.equal(got[7], want[7])
+        assert torch.cuda.current_stream() == side
+    with pytest.raises(ValueError, match="default stream"):
+        sm.mx_quantize(x, sm.MX_FP8, stream=2)
+
+
+def test_a_stream_inside_a_capture():
+    """A step whose product runs on a second stream, captured and replayed."""
+    x, d = (torch.randn(4, 512, device=DEV, generator=gen(124 + i)) for i in range(2))
+    w, _ = random_mx(300, 512, sm.MX_FP4, 126, 116, 120)
+    want = sm.mx_linear(sm.add_rmsnorm(x, d, fmt=sm.MX_FP8).mx, w)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        n = sm.add_rmsnorm(x, d, fmt=sm.MX_FP8)
+        side.wait_stream(torch.cuda.current_stream())
+        y = sm.mx_linear(n.mx, w, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
