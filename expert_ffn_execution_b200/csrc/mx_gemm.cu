@@ -24,6 +24,7 @@
 
 #include "deal.h"
 #include "mx_mma.cuh"
+#include "mx_plan.h"
 #include "tmap.h"
 
 namespace strata {
@@ -378,12 +379,8 @@ cudaError_t launch_gemm(const MxLinearArgs& a, cudaStream_t st) {
 template <int XF, int WF, int DT>
 cudaError_t launch_gemm_rows(const MxLinearArgs& a, cudaStream_t st) {
   constexpr int el = DT == STRATA_DTYPE_F32 ? 4 : 2;
-  // WIDE needs rows on 16-byte boundaries, and is for calls of many rounds of
-  // tiles that take longer to multiply than to store.
   const bool aligned = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy * el % 16 == 0;
-  const int64_t tiles = mx_ceil(a.T, 256) * mx_ceil(a.N, 256);
-  const int chunks = (int)mx_ceil(a.K, GemmCfg<XF, WF, true>::KS);
-  return aligned && tiles > 3 * (a.num_sms / 2) && chunks >= 8
+  return plan_wide(a.T, a.N, a.K, GemmCfg<XF, WF, true>::F4, aligned, a.num_sms)
              ? launch_gemm<XF, WF, DT, true>(a, st)
              : launch_gemm<XF, WF, DT, false>(a, st);
 }

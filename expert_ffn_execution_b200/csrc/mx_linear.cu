@@ -18,10 +18,10 @@
 // orders memory took 5.2 us, and 4.5 us once each CTA sent a rank its tokens
 // by one bulk copy that counts on the receiver's barrier (3.9 us now).
 #include <algorithm>
-#include <cmath>
 
 #include "deal.h"
 #include "mx_mma.cuh"
+#include "mx_plan.h"
 #include "tmap.h"
 
 namespace strata {
@@ -367,50 +367,6 @@ cudaError_t launch_linear(const MxLinearArgs& a, int splits, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = splits > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, wmap, xmap, a, lg, S);
-}
-
-// The form of a call, by what it costs: the stages that a CTA goes through
-// (0.17 to 0.22 us each, most of it the issue of the scale copies and MMAs,
-// so the tile's tokens count for little; half as much again where two CTAs
-// share an SM), the join, reading the sums out.  The factors, in units of about
-// 0.17 us, are fitted to every form's time on 1262 shapes (1 to 1100 tokens, N
-// to 24000, K to 8192, all three pairs of formats): this takes the best form,
-// or one within 8 % of it, for 1251, and is 0.4 % behind on average.
-// Measured, T = 4, 8x4 bits, with 1, 2, 4 and 8 ranks: N = 2560, K = 8192 15.9,
-// 10.1, 7.5 and 6.7 us; N = 8192, K = 2048 6.5, 5.9 and 5.5 with 1, 2 and 4.
-struct LinPlan {
-  int nt, splits;  // tokens a tile, 0: the pairs' tiles; ranks a tile
-};
-LinPlan plan_linear(int T, int N, int K, bool f4, int num_sms) {
-  // Tiles of 16 and 32 tokens are for calls with one: a tile starts at a
-  // multiple of 64 (its scales at a tensor-memory column of their own).
-  const int lo = T <= 16 ? 16 : T <= 32 ? 32 : 64, hi = T <= 64 ? lo : 128;
-  const int chunks = (int)mx_ceil(K, f4 ? 256 : 128);
-  LinPlan best = {0, 1};
-  double least = INFINITY;
-  if (T > 32) {
-    const double rounds = (double)mx_ceil(mx_ceil(T, 256) * mx_ceil(N, 256), num_sms / 2);
-    least = 12 + rounds * (chunks * (f4 ? 2.4 : 1.5) + 3);
-  }
-  for (int nt = lo; nt <= hi; nt *= 2) {
-    const int64_t tiles = mx_ceil(N, kLM) * mx_ceil(T, nt);
-    if (T > 64 && tiles > 5 * num_sms) continue;  // (past what was fitted)
-    for (int s = 1; s <= 8; s *= 2) {
-      const int64_t ctas = tiles * s;
-      // (the sums of 128 tokens twice over leave no room for a second CTA)
-      if (s > 1 && (nt == 128 || ctas > 2 * num_sms || chunks < 2 * s)) break;
-      const bool shared = ctas > num_sms;  // two CTAs an SM
-      double cost = (double)mx_ceil(chunks, s) * (f4 ? 1.5 : 1.0);
-      if (shared) cost = (cost + 1.2) * (1.5 + 0.15 * nt / 64) * (double)mx_ceil(ctas, 2 * num_sms);
-      if (s > 1) cost += 0.2 + 0.14 * nt + (s == 8 && shared ? 1.4 : 0);
-      cost += 0.09 * nt;
-      if (cost < least) {
-        least = cost;
-        best = {nt, s};
-      }
-    }
-  }
-  return best;
 }
 
 template <int XF, int WF>
