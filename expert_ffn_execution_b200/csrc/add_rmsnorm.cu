@@ -13,10 +13,10 @@
 // turn, with the next rows copied ahead, are slower (98 us for 66.9): a row's
 // two reductions are the wait, and many CTAs hide it better than a few.
 //
-// A thread's up to 32 squares are summed in fp32, the threads' sums in fp64
-// (fixed order: warp butterfly, warp partials), which leaves the mean to one
-// rounding: a code next to a border between two then goes the way of the
-// exact norm as often as 32 bits allow.
+// A thread's up to 32 squares are summed in fp32, in two sums, the threads' sums
+// in fp64 (fixed order: warp butterfly, warp partials), and the mean with eps is
+// rounded to fp32 once: a code next to a border between two then goes the way
+// of the exact norm as often as 32 bits allow.
 #include "mx.cuh"
 #include "tc05.cuh"
 
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a
   const int kt = (a.H + 127) / 128;
   const bool tiles = a.fmt && a.layout == STRATA_MX_TILES;
   uint8_t* const scales = a.scales + (tiles ? mx_tile_row(row, kt) : base / kMxBlock);
-  const float inv = rsqrtf((float)sum * a.inv_H + a.eps);
+  const float inv = rsqrtf((float)(sum * a.inv_H + a.eps));
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int g = tid + nth * j;

@@ -278,7 +278,7 @@ struct AddNormArgs {
   int delta_dtype;
   const float* gain;  // or nullptr
   int T, H;
-  float eps, inv_H;
+  double eps, inv_H;
   void* residual_out;  // dtype of x, or nullptr
   void* out;           // or nullptr
   int out_dtype;

@@ -214,7 +214,7 @@ int32_t moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* delta, int32
   a.T = T;
   a.H = H;
   a.eps = eps;
-  a.inv_H = 1.0f / (float)H;
+  a.inv_H = 1.0 / H;
   a.residual_out = residual_out;
   a.out = out;
   a.out_dtype = out_dtype;

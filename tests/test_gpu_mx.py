@@ -961,3 +961,29 @@ def test_a_stream_inside_a_capture():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------- the norm's mean
+@pytest.mark.parametrize("H", [32, 392, 2560, 2592])
+def test_norm_rounds_the_mean_once(H):
+    """Rows of m ones: their squares sum to m exactly, so that the mean has one rounding, m / H's,
+    and the ones become its inverse root as the device's function gives it."""
+    x = torch.ones(H, H, device=DEV).tril()
+    mean = (torch.arange(1, H + 1, device=DEV).double() / H).float()
+    assert torch.equal(sm.add_rmsnorm(x, eps=0.0, out_dtype=torch.float32).out[:, 0], torch.rsqrt(mean))
+
+
+# fp32 steps of h where nothing is added: a sum of up to 16 squares in turn (16 half steps, halved by
+# the root), the mean's one rounding (a half, halved), the device's inverse root (4 half steps), two
+# products (2).
+H_REL_ALONE = (8 + 0.5 + 4 + 2) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("T,H", [(1, 32), (7, 256), (5, 512), (3, 392), (130, 2592), (9481, 1024), (40, 16384)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_alone_is_within_its_steps(dtype, T, H):
+    x = torch.randn(T, H, device=DEV, generator=gen(T + H)).to(dtype)
+    gain = 1 + 0.1 * torch.randn(H, device=DEV, generator=gen(1))
+    h = x.double() / (x.double().pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * gain.double()
+    out = sm.add_rmsnorm(x, gain=gain, out_dtype=torch.float32).out
+    assert ((out.double() - h).abs() <= H_REL_ALONE * h.abs()).all()
