@@ -16,7 +16,12 @@
 // A thread's up to 32 squares are summed in fp32, in two sums, the threads' sums
 // in fp64 (fixed order: warp butterfly, warp partials), and the mean with eps is
 // rounded to fp32 once: a code next to a border between two then goes the way
-// of the exact norm as often as 32 bits allow.
+// of the exact norm as often as 32 bits allow.  A thread whose squares leave
+// fp32's range, or, where eps is too small to cover it, are so small that they
+// lose bits, squares r times a power of two; a row whose mean is out there is
+// taken nearer to one in the same way.  The two checks cost 0 to 4 % (T =
+// 93750, H = 256 19.5 us for 18.8); summing such rows' threads a second time
+// instead takes barriers by number, of which an SM has few (40 us).
 #include "mx.cuh"
 #include "tc05.cuh"
 
@@ -51,6 +56,17 @@ STRATA_DEVFN void store8_as(void* p, int dt, int64_t i, const float (&v)[8]) {
   else
     store8<STRATA_DTYPE_BF16>(reinterpret_cast<uint16_t*>(p) + i, v);
 }
+
+// Whether a sum of squares is one from `least` (its bits) to 2^127: bits order
+// like the numbers, NaN's are above all.
+STRATA_DEVFN bool within(float sum, uint32_t least) {
+  return __float_as_uint(sum) - least <= __float_as_uint(0x1p127f) - least;
+}
+// What brings values whose squares leave fp32's range back into it: below,
+// those of a sum under 2^-90 (r < 2^-43 where a mean is under 2^-100, H <=
+// 2^14) stay under 2^57; above, all stay under 2^58, and what an element loses
+// is below 2^-120 of the row's root mean square.
+STRATA_DEVFN float nearer_to_one(float square) { return square < 1.f ? 0x1p100f : 0x1p-70f; }
 
 // A group of 8 as codes, and its block's scale byte (four adjacent lanes hold
 // a block).
@@ -100,6 +116,17 @@ __global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a
     squares8(r[j], even, odd);
   }
   double sum = (double)even + odd;
+  if (__any_sync(0xffffffffu, !within(even + odd, a.least))) {
+    const float s = within(even + odd, a.least) ? 1.f : nearer_to_one(even + odd);
+    even = odd = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float q[8];
+      scale8(r[j], s, q);
+      squares8(q, even, odd);
+    }
+    sum = ((double)even + odd) * (s < 1.f ? 0x1p140 : s > 1.f ? 0x1p-200 : 1.);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (nth > 32) {
@@ -114,7 +141,15 @@ __global__ void __launch_bounds__(kNMaxThreads) add_rmsnorm_kernel(AddNormArgs a
   const int kt = (a.H + 127) / 128;
   const bool tiles = a.fmt && a.layout == STRATA_MX_TILES;
   uint8_t* const scales = a.scales + (tiles ? mx_tile_row(row, kt) : base / kMxBlock);
-  const float inv = rsqrtf((float)(sum * a.inv_H + a.eps));
+  sum = sum * a.inv_H + a.eps;
+  float mean = (float)sum;
+  if (!within(mean, __float_as_uint(0x1p-100f))) {
+    const float s = nearer_to_one(mean);  // h is also that of r s and eps s^2
+    mean = (float)(sum * s * s);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) scale8(r[j], s, r[j]);
+  }
+  const float inv = rsqrtf(mean);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int g = tid + nth * j;

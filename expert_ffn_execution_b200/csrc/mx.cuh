@@ -279,6 +279,7 @@ struct AddNormArgs {
   const float* gain;  // or nullptr
   int T, H;
   double eps, inv_H;
+  uint32_t least;      // bits of the least sum of squares of a thread that loses none
   void* residual_out;  // dtype of x, or nullptr
   void* out;           // or nullptr
   int out_dtype;

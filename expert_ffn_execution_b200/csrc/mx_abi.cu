@@ -215,6 +215,8 @@ int32_t moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* delta, int32
   a.H = H;
   a.eps = eps;
   a.inv_H = 1.0 / H;
+  // squares lose at most 2^-150 each: 2^-55 of such a sum, 2^-50 of such an eps
+  a.least = eps < 0x1p-100f ? (127u - 90u) << 23 : 0u;
   a.residual_out = residual_out;
   a.out = out;
   a.out_dtype = out_dtype;

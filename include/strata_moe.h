@@ -461,6 +461,8 @@ STRATA_API int32_t moe_mx_tile_scales(const void* scales, int32_t rows, int32_t 
  *   out = h            (out_dtype; NULL: not written)
  *   codes, scales = the MX form of h   (mx_fmt 0: not written)
  * The norm is of r before its rounding to the dtype of x.
+ * Squares may leave fp32's range: a finite row of any magnitude has its h; an
+ * infinite element makes itself NaN and the rest of its row 0.
  *   x [T,H], delta [T,H] or NULL: F32 / F16 / BF16;  gain fp32 [H] or NULL
  *   (unit gain).  At least one of residual_out, out and the MX form is
  *   written.  Where codes are written, scales [T, H/32] go in scale_layout.

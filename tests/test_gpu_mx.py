@@ -987,3 +987,51 @@ def test_norm_alone_is_within_its_steps(dtype, T, H):
     h = x.double() / (x.double().pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * gain.double()
     out = sm.add_rmsnorm(x, gain=gain, out_dtype=torch.float32).out
     assert ((out.double() - h).abs() <= H_REL_ALONE * h.abs()).all()
+
+
+# rows whose squares leave fp32's range, above and below: (largest magnitude, eps)
+FAR = [(2.0 ** 127, 1e-6), (1e30, 1e-6), (3e19, 0.0), (2.0 ** 60, 1e-6), (1e-12, 0.0), (1e-25, 0.0), (1e-38, 0.0),
+       (2.0 ** -140, 0.0), (1e-25, 1e-50), (1e-18, 1e-36), (1e-25, 1e-6)]
+
+
+@pytest.mark.parametrize("T,H", [(1, 32), (7, 256), (5, 512), (6, 1024), (131, 2592), (3, 16384)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_of_rows_far_from_one(dtype, T, H):
+    """h is about one whatever the rows' magnitude; neighbours in a CTA are ordinary rows.  Rows of
+    2^-140 are subnormals: what they are is exact, and so is all that is done to them."""
+    x = torch.randn(T, H, device=DEV, generator=gen(T + H)).clamp(-3, 3)
+    gain = 1 + 0.1 * torch.randn(H, device=DEV, generator=gen(1))
+    for size, eps in FAR:
+        far = x.clone()
+        far[::2] *= size / 4
+        far = far.to(dtype)
+        if eps == 0 and not far.any(1).all():
+            continue  # bf16 has nothing that small
+        eps32 = torch.tensor(eps, dtype=torch.float32).double().item()
+        h = far.double() / (far.double().pow(2).mean(-1, keepdim=True) + eps32).sqrt() * gain.double()
+        n = sm.add_rmsnorm(far, gain=gain, eps=eps, out_dtype=torch.float32, fmt=sm.MX_FP8)
+        assert n.out.isfinite().all()
+        # (an element 2^56 below a row of 2^61 and more may lose its last bits: below 2^-120 of h)
+        assert ((n.out.double() - h).abs() <= H_REL_ALONE * h.abs() + 2.0 ** -120).all(), (size, eps)
+        q = sm.mx_quantize(n.out, sm.MX_FP8)
+        assert torch.equal(n.mx.codes, q.codes) and torch.equal(n.mx.scales, q.scales)
+
+
+def test_norm_of_mixed_and_infinite_rows():
+    """One large element among ordinary ones; an infinite one makes its row 0 and itself NaN, as the
+    formula has it; rows of zeros without eps are 0 / 0."""
+    H = 1024
+    x = torch.randn(6, H, device=DEV, generator=gen(3))
+    x[0, 5] = 1e30
+    x[1, 7] = float("inf")
+    x[2] = 0
+    x[3, 9] = -float("inf")
+    x[3, 8] = float("nan")
+    n = sm.add_rmsnorm(x, eps=0.0, out_dtype=torch.float32, fmt=sm.MX_FP4)
+    h = x[0].double() / x[0].double().pow(2).mean().sqrt()
+    assert ((n.out[0].double() - h).abs() <= H_REL_ALONE * h.abs() + 2.0 ** -120).all()
+    assert n.out[1, 7].isnan() and (torch.cat([n.out[1, :7], n.out[1, 8:]]) == 0).all()
+    assert n.out[2].isnan().all() and n.out[3].isnan().all()
+    assert torch.equal(n.out[4:], sm.add_rmsnorm(x[4:].clone(), eps=0.0, out_dtype=torch.float32).out)
+    v = n.mx.dequantize()
+    assert v[1, :32].isnan().all() and (v[1, 32:] == 0).all() and v[2:4].isnan().all() and v[4:].isfinite().all()
