@@ -220,7 +220,7 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t st) {
   // only read are bound by instructions, four save more of them (T = 23437:
   // 24.1, 20.0 and 18.0 us with one, two and four), and fp32 rows with a
   // delta by HBM (T = 5859, H = 4096: 48.7, 49.2 and 52.7 us).
-  const int64_t filled = (int64_t)148 * 64 * 32;
+  const int64_t filled = (int64_t)a.num_sms * 64 * 32;
   int vpt = 1;
   if (G > 32 && groups > filled / 2) vpt = 2;
   if (vpt == 2 && groups > 4 * filled)

@@ -287,6 +287,7 @@ struct AddNormArgs {
   uint8_t* codes;
   uint8_t* scales;
   int layout;
+  int num_sms;
 };
 cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t st);
 

@@ -224,6 +224,7 @@ int32_t moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* delta, int32
   a.codes = reinterpret_cast<uint8_t*>(codes);
   a.scales = reinterpret_cast<uint8_t*>(scales);
   a.layout = scale_layout;
+  a.num_sms = num_sms_of_current_device();
   return from_cuda(launch_add_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
