@@ -2,7 +2,8 @@
 
 Each .cu under csrc/ is compiled to an object (in parallel) and linked into one
 shared library next to this file; native/mxcalls.cpp becomes the Python module
-_mxcalls beside it (g++, the CPython and torch headers).  Run `python -m expert_ffn_execution_b200.build`.
+_mxcalls beside it (g++, the CPython and torch headers), where it can be built:
+without it the same calls run in Python.  Run `python -m expert_ffn_execution_b200.build`.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libstrata_moe.so")
 CALLS_SRC = os.path.join(HERE, "native", "mxcalls.cpp")
-CALLS = os.path.join(HERE, "_mxcalls.so")
+# named for this interpreter: another's neither finds it nor takes it for its own
+CALLS = os.path.join(HERE, "_mxcalls" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -59,7 +62,10 @@ def up_to_date() -> bool:
 
 
 def build_calls(force: bool = False) -> str:
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    torch_dir = os.path.dirname(spec.origin)
     deps = (CALLS_SRC, os.path.join(INCLUDE, "strata_moe.h"), os.path.join(torch_dir, "version.py"))
     if not force and os.path.exists(CALLS) and all(
             os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
@@ -81,8 +87,29 @@ def build_calls(force: bool = False) -> str:
     return CALLS
 
 
+def try_build_calls(force: bool = False) -> str | None:
+    """The native module or, where it cannot be built (no compiler, no Python
+    headers, a torch without CUDA or with other headers), None and a warning."""
+    # an older build's name, which any interpreter would import
+    for old in {os.path.join(HERE, "_mxcalls.so")} - {CALLS}:
+        if os.path.exists(old):
+            os.remove(old)
+    try:
+        return build_calls(force)
+    except Exception as e:  # whatever is missing: the module is optional
+        if os.path.exists(CALLS):
+            os.remove(CALLS)  # of other sources or another torch
+        warnings.warn(f"_mxcalls was not built, the microscaled calls run in Python: {e}")
+        return None
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    build_calls(force)
+    lib = build_library(force, verbose_ptxas)
+    try_build_calls(force)
+    return lib
+
+
+def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -306,3 +306,36 @@ def test_matrix_follows_its_tensors(plain):
     r = subprocess.run([sys.executable, "-c", HELD.format(plain=plain)], capture_output=True, text=True,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr
+
+
+# ---------------------------------------------------------------- the native module's build
+@pytest.mark.parametrize("missing", ["compiler", "torch"])
+def test_library_is_built_where_the_native_module_is_not(monkeypatch, tmp_path, missing):
+    """No compiler for it, no torch: a warning, the library all the same, and
+    no module of other sources left behind."""
+    from expert_ffn_execution_b200 import build
+    calls = tmp_path / "_mxcalls.so"
+    calls.write_bytes(b"old")
+    monkeypatch.setattr(build, "CALLS", str(calls))
+    monkeypatch.setattr(build, "HERE", str(tmp_path))
+    os.utime(calls, (0, 0))
+    if missing == "compiler":
+        monkeypatch.setenv("CXX", "/bin/false")
+    else:
+        monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: None)
+    with pytest.warns(UserWarning, match="_mxcalls was not built"):
+        assert build.build() == build.LIB
+    assert os.path.exists(build.LIB) and not calls.exists()
+
+
+def test_native_module_is_this_interpreters(monkeypatch, tmp_path):
+    """Named so that no other interpreter imports it; one under the name that
+    any would import goes."""
+    import importlib.machinery
+    from expert_ffn_execution_b200 import build
+    assert os.path.basename(build.CALLS) == "_mxcalls" + importlib.machinery.EXTENSION_SUFFIXES[0]
+    (tmp_path / "_mxcalls.so").write_bytes(b"old")
+    monkeypatch.setattr(build, "HERE", str(tmp_path))
+    monkeypatch.setattr(build, "build_calls", lambda force: "built")
+    assert build.try_build_calls() == "built"
+    assert not (tmp_path / "_mxcalls.so").exists()
