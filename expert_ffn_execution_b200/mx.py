@@ -59,6 +59,9 @@ def _dtype(dtype) -> int:
 def _device(first, *others):
     """The one CUDA device of the tensors (None among the others is passed over)."""
     dev = first.device
+    for t in (first, *others):
+        if isinstance(t, torch.Tensor) and t.is_neg():
+            raise ValueError("a view that negates its memory: see Tensor.resolve_neg()")
     if dev.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device")
     for t in others:

@@ -339,3 +339,21 @@ def test_native_module_is_this_interpreters(monkeypatch, tmp_path):
     monkeypatch.setattr(build, "build_calls", lambda force: "built")
     assert build.try_build_calls() == "built"
     assert not (tmp_path / "_mxcalls.so").exists()
+
+
+def test_negated_views_are_refused():
+    """The calls read memory, and a lazily negated view is not what its memory holds."""
+    x = torch.zeros(4, 64)
+    n = torch._neg_view(x)
+    w, d = torch.zeros(2, 128, 256), torch.zeros(2, 256, 128)
+    q = sm.MXTensor(torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), sm.MX_FP8, 4, 128,
+                    sm.MX_TILES)
+    r = sm.MXTensor(q.codes[:1], q.scales, sm.MX_FP8, 1, 128, sm.MX_TILES)
+    bias = torch.zeros(1, dtype=torch.complex64).conj().imag
+    assert bias.is_neg() and bias.is_contiguous()
+    for call in (lambda: sm.mx_quantize(n, sm.MX_FP8), lambda: sm.add_rmsnorm(n, fmt=sm.MX_FP8),
+                 lambda: sm.add_rmsnorm(x, n, fmt=sm.MX_FP8), lambda: sm.mx_linear(q, r, bias),
+                 lambda: sm.mx_linear(q, q, out=torch._neg_view(x[:, :4].contiguous())),
+                 lambda: sm.pack_experts(w, torch._neg_view(w), d)):
+        with pytest.raises(ValueError, match="negates"):
+            call()
