@@ -212,21 +212,29 @@ class MXTensor(_Matrix):
 
 def _scales_at(q: MXTensor) -> int:
     """Where the scales are in one allocation of both planes."""
-    return (_code_bytes(q.rows, q.fmt, q.K) + 255) & ~255
+    return (_code_bytes(q._rows, q._fmt, q._K) + 255) & ~255
 
 
 def _planes(q: MXTensor):
     """Where the codes and the scales are now.  The tensors may have been given
     other memory since the last call (`t.data = ...`, Module.to())."""
     codes, scales = q._codes, q._scales
-    for t, n, what in ((codes, _code_bytes(q.rows, q.fmt, q.K), "codes"),
-                       (scales, _scale_bytes(q.rows, q.K, q.layout), "scales")):
-        if t is not None and (t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n):
-            raise ValueError(f"{what} must be contiguous uint8 of {n} bytes")
-    a, b = (q._both if t is None else t for t in (codes, scales))
-    if a.device != b.device:
-        raise ValueError(f"codes on {a.device} and scales on {b.device}")
-    return a.data_ptr(), b.data_ptr() + (_scales_at(q) if scales is None else 0)
+    if codes is None and scales is None:
+        at = q._both.data_ptr()
+        return at, at + _scales_at(q)
+    n = _code_bytes(q._rows, q._fmt, q._K)
+    if codes is None:
+        codes = q._both
+    elif codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.numel() != n:
+        raise ValueError(f"codes must be contiguous uint8 of {n} bytes")
+    n, at = _scale_bytes(q._rows, q._K, q._layout), 0
+    if scales is None:
+        scales, at = q._both, _scales_at(q)
+    elif scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.numel() != n:
+        raise ValueError(f"scales must be contiguous uint8 of {n} bytes")
+    if codes.device != scales.device:
+        raise ValueError(f"codes on {codes.device} and scales on {scales.device}")
+    return codes.data_ptr(), scales.data_ptr() + at
 
 
 def mx_quantize(x: torch.Tensor, fmt: int, layout: int = B.MX_TILES, stream=None) -> MXTensor:
