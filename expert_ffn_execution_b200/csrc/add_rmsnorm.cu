@@ -6,11 +6,11 @@
 // A row is one CTA's, or one or two warps' of a CTA of 128 threads, and stays
 // in registers between the sum of squares and the output, so every input is
 // read once and every output written once: bound by HBM for many rows (T =
-// 8192, H = 4096, fp32 + bf16 to bf16 and FP8: 66.9 us, 6.5 TB/s), by
+// 8192, H = 4096, fp32 + bf16 to bf16 and FP8: 66.0 us, 6.6 TB/s), by
 // instructions where a row is only read and its codes written (126 a group of
-// 8 elements and warp; T = 5859, H = 4096, bf16 to FP4: 19.8 us), by the
+// 8 elements and warp; T = 5859, H = 4096, bf16 to FP4: 18.6 us), by the
 // launch and one load-reduce-store chain for few.  CTAs that take rows in
-// turn, with the next rows copied ahead, are slower (98 us for 66.9): a row's
+// turn, with the next rows copied ahead, are slower (98 us for 66.0): a row's
 // two reductions are the wait, and many CTAs hide it better than a few.
 //
 // A thread's up to 32 squares are summed in fp32, in two sums, the threads' sums
@@ -19,9 +19,10 @@
 // of the exact norm as often as 32 bits allow.  A thread whose squares leave
 // fp32's range, or, where eps is too small to cover it, are so small that they
 // lose bits, squares r times a power of two; a row whose mean is out there is
-// taken nearer to one in the same way.  The two checks cost 0 to 4 % (T =
-// 93750, H = 256 19.5 us for 18.8); summing such rows' threads a second time
-// instead takes barriers by number, of which an SM has few (40 us).
+// taken nearer to one in the same way.  The two checks and the mean in fp64 cost
+// 0 to 3 % (T = 93750, H = 256 21.4 us for 20.7, T = 8192 nothing) and 0.1 us of
+// a few rows' 2.0; summing such rows' threads a second time instead takes
+// barriers by number, of which an SM has few (40 us for T = 93750).
 #include "mx.cuh"
 #include "tc05.cuh"
 
@@ -214,25 +215,25 @@ cudaError_t launch_add_rmsnorm(const AddNormArgs& a, cudaStream_t st) {
   const int G = a.H / 8;
   const int64_t groups = (int64_t)a.T * G;
   // Groups a thread: one where that leaves SMs half empty (a thread's chain is
-  // the time: T = 234, H = 1024, bf16 to FP4 2.2 us, with two 2.4) and for
+  // the time: T = 234, H = 1024, bf16 to FP4 2.0 us, with two 2.3) and for
   // rows of one warp; else two, which share a thread's fixed part (T = 2343:
-  // 4.0 and 3.4 us).  With the SMs filled several times over, rows that are
+  // 4.0 and 3.6 us).  With the SMs filled several times over, rows that are
   // only read are bound by instructions, four save more of them (T = 23437:
-  // 24.1, 20.0 and 18.0 us with one, two and four), and fp32 rows with a
-  // delta by HBM (T = 5859, H = 4096: 48.7, 49.2 and 52.7 us).
+  // 23.5, 19.0 and 17.0 us with one, two and four), and fp32 rows with a
+  // delta by HBM (T = 5859, H = 4096: 48.1, 49.0 and 50.7 us).
   const int64_t filled = (int64_t)a.num_sms * 64 * 32;
   int vpt = 1;
   if (G > 32 && groups > filled / 2) vpt = 2;
   if (vpt == 2 && groups > 4 * filled)
     vpt = !a.delta ? (G > 64 ? 4 : 2) : a.x_dtype == STRATA_DTYPE_F32 ? 1 : 2;
   // threads of a row, whole warps; not an eighth more idle ones than with half
-  // of the groups (H = 1536, four groups: 22.2 us, two: 20 us)
+  // of the groups (T = 15625, H = 1536, four groups: 21.5 us, two: 19.1 us)
   auto threads_of = [&](int v) { return ((G + v - 1) / v + 31) & ~31; };
   while (vpt > 1 && 8 * vpt * threads_of(vpt) > 9 * (vpt / 2) * threads_of(vpt / 2)) vpt /= 2;
   while (G > vpt * kNMaxThreads) vpt *= 2;
   const int threads = threads_of(vpt);
   // up to 128 threads a CTA, then a CTA a row (T = 93750, H = 256, bf16 to
-  // FP4: 22 us with four rows a CTA, 51 with one)
+  // FP4: 21 us with four rows a CTA, 50 with one)
   int per = 1;
   while (2 * per * threads <= 128) per *= 2;
   const dim3 block(threads, per);

@@ -14,9 +14,13 @@ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // (0.17 to 0.22 us each, most of it the issue of the scale copies and MMAs,
 // so the tile's tokens count for little; half as much again where two CTAs
 // share an SM), the join, reading the sums out.  The factors, in units of about
-// 0.17 us, are fitted to every form's time on 1262 shapes (1 to 1100 tokens, N
-// to 24000, K to 8192, all three pairs of formats): this takes the best form,
-// or one within 8 % of it, for 1251, and is 0.4 % behind on average.
+// 0.17 us, are fitted to every form's time on shapes of 1 to 1100 tokens, N to
+// 24000, K to 8192 in all three pairs of formats.  On the 1238 of them that
+// profiles/mx_linear_forms.csv lists this takes the best form, or one within 8 %
+// of it, for 1227, and is 0.4 % behind on average.  Larger N is not fitted:
+// past 5 tiles an SM calls of more than 64 tokens go to the pairs, half or more
+// of whose 256 tokens are then padding (N = 128256, K = 4096, 8x4 bits: 64 us
+// for 64 tokens, 85 for 65, 104 for 256).
 // Measured, T = 4, 8x4 bits, with 1, 2, 4 and 8 ranks: N = 2560, K = 8192 15.9,
 // 10.1, 7.5 and 6.7 us; N = 8192, K = 2048 6.5, 5.9 and 5.5 with 1, 2 and 4.
 struct LinPlan {

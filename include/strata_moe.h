@@ -457,7 +457,7 @@ STRATA_API int32_t moe_mx_tile_scales(const void* scales, int32_t rows, int32_t 
 
 /* The residual's addition and the norm that follows it:
  *   r = x + delta,  h = r / sqrt(mean(r^2) + eps) * gain    (fp32)
- *   residual_out = r   (dtype of x; NULL: not written; may alias x)
+ *   residual_out = r   (dtype of x; NULL: not written; may be x itself)
  *   out = h            (out_dtype; NULL: not written)
  *   codes, scales = the MX form of h   (mx_fmt 0: not written)
  * The norm is of r before its rounding to the dtype of x.
@@ -468,7 +468,9 @@ STRATA_API int32_t moe_mx_tile_scales(const void* scales, int32_t rows, int32_t 
  *   written.  Where codes are written, scales [T, H/32] go in scale_layout.
  * Limits: T >= 0 (0: no-op), H in 32..16384, a multiple of 8, of 32 where
  * codes are written.  All pointers 16-byte aligned (scales by rows: any).
- * The sum of squares is taken in a fixed order: the same bits on every run. */
+ * Outputs overlap neither one another nor, but for residual_out as x, an input.
+ * The sum of squares is taken in an order that depends on T, H, the types and
+ * the device alone: the same bits on every run. */
 STRATA_API int32_t moe_add_rmsnorm(const void* x, int32_t x_dtype, const void* delta,
                         int32_t delta_dtype, const float* gain, int32_t T, int32_t H, float eps,
                         void* residual_out, void* out, int32_t out_dtype, int32_t mx_fmt,
